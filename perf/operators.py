@@ -132,8 +132,8 @@ def plain_encode(w):
     of BF16 w [.., rows, cols].  A group's scale is 2^(e - 127), the smallest
     (e >= 1) that keeps every |w| within 7 of it, so that no weight moves by
     more than half of the largest step between two codes; weights round to the
-    nearest of the 16 values, ties to the even code.  A group that holds an
-    infinity or a NaN gets e = 255."""
+    nearest of the 16 values that BF16 holds, ties to the even code.  A group
+    that holds an infinity or a NaN gets e = 255."""
     cols = w.shape[-1]
     groups = -(-cols // GROUP)
     f = torch.nn.functional.pad(w.float(), (0, groups * GROUP - cols))
@@ -145,6 +145,7 @@ def plain_encode(w):
     a = f.abs() * ((254 - e) << 23).view(torch.float32)[..., None]  # |w| / 2^(e - 127), exact
     code = ((a > 0.25).int() + (a >= 0.75).int() + (a > 1.25).int() + (a >= 1.75).int()
             + (a > 2.5).int() + (a >= 3.5).int() + (a > 5).int())
+    code = torch.where(e[..., None] == 253, code.clamp(max=5), code)  # 4 * 2^126 is past BF16
     code = code | torch.signbit(f).int() << 3
     bad = top >= 0x7F80
     e = torch.where(bad, 255, e)

@@ -9,6 +9,11 @@ into GEMV (page "Compresión de pesos LLM sin pérdida vs 8-bit GGUF: ¿qué est
 listo para producción?", section "¿Qué significa “sin pérdida” para los pesos
 de un LLM?").
 
+Next to it a 4-bit tier that loses precision, for tensors that 12 bits per
+weight leave too large (fp4_encode, fp4_decode, fp4_gemv; include/wc_fp4.h),
+and a mixture-of-experts layer for a few tokens on BF16 or 4-bit experts
+(moe; include/wc_moe.h).
+
 This module only marshals arguments: every step runs in the HIP kernels of
 libwc.so, on the caller's current torch stream.  PyTorch provides device
 memory and streams.  There is no CPU fallback: importing this package
@@ -18,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch  # loaded first, so libwc binds to the HIP runtime torch already uses
 
@@ -26,6 +32,7 @@ __all__ = [
     "encode", "decode", "decode_gemv", "gemv_bf16", "bits_per_weight", "read_header",
     "crc32", "container_crcs", "artifact_write", "artifact_entries", "artifact_read",
     "artifact_verify", "LIB_PATH",
+    "Fp4", "fp4_encode", "fp4_decode", "fp4_gemv", "SOFTMAX", "SIGMOID", "moe", "moe_workspace_bytes",
 ]
 
 BYTESPLIT = 0
@@ -83,6 +90,17 @@ class ArtifactInfo(ctypes.Structure):
     ]
 
 
+class MoeShape(ctypes.Structure):
+    """wc_moe_shape (include/wc_moe.h)."""
+    _fields_ = [(n, ctypes.c_uint32) for n in ("tokens", "hidden", "inter", "experts", "top_k",
+                                               "scoring", "flags")] + [("scale", ctypes.c_float)]
+
+
+class MoeExperts(ctypes.Structure):
+    """wc_moe_experts (include/wc_moe.h)."""
+    _fields_ = [("kind", ctypes.c_uint32), ("data", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
 def _load(path: str = LIB_PATH):
     if not os.path.exists(path):
         raise ImportError(
@@ -109,7 +127,15 @@ def _load(path: str = LIB_PATH):
     lib.wc_artifact_entry.argtypes = [ctypes.c_char_p, ctypes.c_uint32,
                                       ctypes.POINTER(ArtifactInfo)]
     lib.wc_artifact_read.argtypes = [ctypes.c_char_p, ctypes.c_uint32, P, ctypes.c_size_t]
-    for f in (lib.wc_build_dict, lib.wc_encode, lib.wc_encode_noalloc, lib.wc_decode, lib.wc_decode_gemv,
+    lib.wc_fp4_encode.argtypes = [P, U64, U64, P, P, P]
+    lib.wc_fp4_decode.argtypes = [P, P, U64, U64, P, P]
+    lib.wc_fp4_gemv.argtypes = [P, P, U64, U64, P, ctypes.c_uint32, P, P]
+    lib.wc_moe_workspace_bytes.argtypes = [ctypes.POINTER(MoeShape)]
+    lib.wc_moe_workspace_bytes.restype = ctypes.c_size_t
+    EP = ctypes.POINTER(MoeExperts)
+    lib.wc_moe.argtypes = [ctypes.POINTER(MoeShape), P, P, P, EP, EP, P, P, P, P, ctypes.c_size_t, P]
+    for f in (lib.wc_fp4_encode, lib.wc_fp4_decode, lib.wc_fp4_gemv, lib.wc_moe,
+              lib.wc_build_dict, lib.wc_encode, lib.wc_encode_noalloc, lib.wc_decode, lib.wc_decode_gemv,
               lib.wc_gemv_bf16, lib.wc_bits_per_weight, lib.wc_container_crcs,
               lib.wc_artifact_write, lib.wc_artifact_count, lib.wc_artifact_entry,
               lib.wc_artifact_read):
@@ -422,3 +448,187 @@ def artifact_verify(path: str, device="cuda:0"):
         bpw = bits_per_weight(h)[0] if h.n else 0.0
         out.append((e["name"], got == e["src_crc"], bpw))
     return out
+
+
+# ---- 4-bit weights with group scales (include/wc_fp4.h) ----------------------
+
+FP4_GROUP = 32          # columns that share a scale
+FP4_MAX_COLS = 1 << 24  # WC_FP4_MAX_COLS
+
+
+class Fp4(NamedTuple):
+    """A BF16 matrix [rows, cols], or a stack of them [n, rows, cols], as
+    4-bit codes: codes uint8 [.., rows, 16 G] and scales uint8 [.., rows, G]
+    with G = ceil(cols / 32) groups per row."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    cols: int
+
+
+def _fp4(q: Fp4, what: str):
+    """(leading dims, rows, cols) of a checked Fp4."""
+    codes, scales, cols = q
+    for t, name in ((codes, "codes"), (scales, "scales")):
+        if not _on_device(t):
+            raise ValueError(f"{what}.{name} must be a device tensor")
+        if t.dtype != torch.uint8:
+            raise TypeError(f"{what}.{name} must be a uint8 tensor")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}.{name} must be contiguous")
+    cols = int(cols)
+    shape = tuple(scales.shape)
+    if cols < 0 or len(shape) not in (2, 3) or shape[-1] != (cols + FP4_GROUP - 1) // FP4_GROUP:
+        raise ValueError(f"{what}.scales has shape {shape}, expected [.., rows, "
+                         f"{(cols + FP4_GROUP - 1) // FP4_GROUP}] for {cols} columns")
+    if tuple(codes.shape) != shape[:-1] + (16 * shape[-1],):
+        raise ValueError(f"{what}.codes has shape {tuple(codes.shape)}, expected "
+                         f"{shape[:-1] + (16 * shape[-1],)}")
+    return shape[:-2], shape[-2], cols
+
+
+def _used_on(stream, *tensors):
+    """Memory allocated here on the current stream and used on another one is
+    not handed out again before that one is done with it."""
+    if stream is not None and stream != torch.cuda.current_stream():
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def fp4_encode(w: torch.Tensor, out: Fp4 | None = None, stream=None) -> Fp4:
+    """wc_fp4_encode: w [rows, cols] or [n, rows, cols], BF16, as 4-bit codes."""
+    w = _bits16(w, "w")
+    if w.dim() not in (2, 3):
+        raise ValueError(f"w must be [rows, cols] or [n, rows, cols], got {tuple(w.shape)}")
+    cols = w.shape[-1]
+    groups = (cols + FP4_GROUP - 1) // FP4_GROUP
+    if out is None:
+        out = Fp4(torch.empty((*w.shape[:-1], 16 * groups), dtype=torch.uint8, device=w.device),
+                  torch.empty((*w.shape[:-1], groups), dtype=torch.uint8, device=w.device), cols)
+        _used_on(stream, out.codes, out.scales)
+    _fp4(out, "out")
+    if tuple(out.scales.shape) != (*w.shape[:-1], groups) or out.cols != cols:
+        raise ValueError(f"out holds {tuple(out.scales.shape[:-1])} rows of {out.cols} columns, "
+                         f"w has shape {tuple(w.shape)}")
+    _same_device("fp4_encode", w, out.codes, out.scales)
+    _check(_lib.wc_fp4_encode(_ptr(w), w.shape[:-1].numel(), cols, _ptr(out.codes),
+                              _ptr(out.scales), _stream(stream)), "wc_fp4_encode")
+    return out
+
+
+def fp4_decode(q: Fp4, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """wc_fp4_decode: the BF16 values that q stands for, [.., rows, cols]."""
+    lead, rows, cols = _fp4(q, "q")
+    shape = (*lead, rows, cols)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.codes.device)
+        _used_on(stream, out)
+    out = _bits16(out, "out")
+    if tuple(out.shape) != shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
+    _same_device("fp4_decode", q.codes, q.scales, out)
+    _check(_lib.wc_fp4_decode(_ptr(q.codes), _ptr(q.scales), out.shape[:-1].numel(), cols,
+                              _ptr(out), _stream(stream)), "wc_fp4_decode")
+    return out
+
+
+def fp4_gemv(q: Fp4, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """wc_fp4_gemv: y [batch, rows] fp32 for x [batch, cols] BF16."""
+    lead, rows, cols = _fp4(q, "q")
+    if lead:
+        raise ValueError(f"q must be one matrix, got a stack of {lead[0]}")
+    x = _bits16(x, "x")
+    batch = _batch_of(x, cols)
+    if out is None:
+        out = torch.empty((batch, rows), dtype=torch.float32, device=x.device)
+        _used_on(stream, out)
+    _gemv_out(out, batch, rows)
+    _same_device("fp4_gemv", q.codes, q.scales, x, out)
+    _check(_lib.wc_fp4_gemv(_ptr(q.codes), _ptr(q.scales), rows, cols, _ptr(x), batch, _ptr(out),
+                            _stream(stream)), "wc_fp4_gemv")
+    return out
+
+
+# ---- mixture of experts (include/wc_moe.h) -----------------------------------
+
+SOFTMAX = 0
+SIGMOID = 1
+MOE_RENORM = 1  # WC_MOE_RENORM
+MOE_MAX_TOKENS = 64
+
+
+def _moe_shape(tokens, hidden, inter, experts, top_k, scoring, renorm, scale) -> MoeShape:
+    return MoeShape(tokens, hidden, inter, experts, top_k, scoring, MOE_RENORM if renorm else 0,
+                    scale)
+
+
+def moe_workspace_bytes(tokens: int, hidden: int, inter: int, experts: int, top_k: int) -> int:
+    """wc_moe_workspace_bytes: device scratch of one moe call of that shape."""
+    need = _lib.wc_moe_workspace_bytes(
+        ctypes.byref(_moe_shape(tokens, hidden, inter, experts, top_k, SOFTMAX, True, 1.0)))
+    if need == 0:
+        raise WCError(-5, "wc_moe_workspace_bytes")
+    return need
+
+
+def _moe_experts(w, rows, cols, experts, what):
+    """(wc_moe_experts, its tensors) of a stack [experts, rows, cols]."""
+    if isinstance(w, Fp4):
+        lead, r, c = _fp4(w, what)
+        shape, tensors = (*lead, r, c), (w.codes, w.scales)
+    else:
+        shape, tensors = tuple(_bits16(w, what).shape), (w,)
+    if shape != (experts, rows, cols):
+        raise ValueError(f"{what} has shape {shape}, expected {(experts, rows, cols)}")
+    return MoeExperts(len(tensors) - 1, *(_ptr(t) for t in tensors)), tensors
+
+
+def moe(x: torch.Tensor, router: torch.Tensor, gate_up, down, top_k: int, *, scoring: int = SOFTMAX,
+        bias: torch.Tensor | None = None, renorm: bool = True, scale: float = 1.0,
+        work: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None):
+    """wc_moe: (y [tokens, hidden] BF16, ids [tokens, top_k] int32, weights
+    [tokens, top_k] fp32) of a mixture-of-experts layer for up to 64 tokens.
+
+    x [tokens, hidden] and router [experts, hidden] BF16; gate_up
+    [experts, 2 * inter, hidden] and down [experts, hidden, inter], each BF16 or
+    Fp4; bias fp32 [experts], added to the scores for the choice only (-inf
+    takes an expert out).  work: uint8, moe_workspace_bytes(..) of it; a call
+    with the same one on another stream must not overlap."""
+    x, router = _bits16(x, "x"), _bits16(router, "router")
+    if x.dim() != 2 or router.dim() != 2 or x.shape[1] != router.shape[1]:
+        raise ValueError(f"x must be [tokens, hidden] and router [experts, hidden], got "
+                         f"{tuple(x.shape)} and {tuple(router.shape)}")
+    (tokens, hidden), experts = x.shape, router.shape[0]
+    if not 1 <= tokens <= MOE_MAX_TOKENS:
+        raise ValueError(f"{tokens} tokens outside 1..{MOE_MAX_TOKENS}")
+    dshape = down.scales.shape[:-1] + (down.cols,) if isinstance(down, Fp4) else down.shape
+    if len(dshape) != 3:
+        raise ValueError(f"down must be a stack [experts, hidden, inter], got {tuple(dshape)}")
+    inter = int(dshape[-1])
+    cgu, tgu = _moe_experts(gate_up, 2 * inter, hidden, experts, "gate_up")
+    cdn, tdn = _moe_experts(down, hidden, inter, experts, "down")
+    if bias is not None:
+        if not _on_device(bias):
+            raise ValueError("bias must be a device tensor")
+        if bias.dtype != torch.float32:
+            raise TypeError("bias must be float32")
+        if tuple(bias.shape) != (experts,) or not bias.is_contiguous():
+            raise ValueError(f"bias must be a contiguous [{experts}], got {tuple(bias.shape)}")
+    shape = _moe_shape(tokens, hidden, inter, experts, top_k, scoring, renorm, scale)
+    need = _lib.wc_moe_workspace_bytes(ctypes.byref(shape))
+    if work is None:
+        work = torch.empty(need, dtype=torch.uint8, device=x.device)
+        _used_on(stream, work)
+    _bytes(work, "work", need)
+    if out is None:
+        out = torch.empty((tokens, hidden), dtype=torch.bfloat16, device=x.device)
+        _used_on(stream, out)
+    if tuple(_bits16(out, "out").shape) != (tokens, hidden):
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(tokens, hidden)}")
+    ids = torch.empty((tokens, top_k), dtype=torch.int32, device=x.device)
+    weights = torch.empty((tokens, top_k), dtype=torch.float32, device=x.device)
+    _used_on(stream, ids, weights)
+    _same_device("moe", x, router, work, out, *tgu, *tdn, *(() if bias is None else (bias,)))
+    _check(_lib.wc_moe(ctypes.byref(shape), _ptr(x), _ptr(router), _ptr(bias), ctypes.byref(cgu),
+                       ctypes.byref(cdn), _ptr(out), _ptr(ids), _ptr(weights), _ptr(work),
+                       work.numel(), _stream(stream)), "wc_moe")
+    return out, ids, weights

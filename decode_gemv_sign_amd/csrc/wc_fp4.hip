@@ -57,7 +57,8 @@ __global__ __launch_bounds__(kBlockThreads) void k_fp4_encode(const uint16_t* __
   for (uint64_t p = (uint64_t)blockIdx.x * kBlockThreads + threadIdx.x; p < total; p += stride) {
     const uint64_t row = p / (groups * 4u);
     const uint32_t c = (uint32_t)(p - row * (groups * 4u)) * 8u;
-    const u32x4 v = load8(w + row * cols + c, (int)cols - (int)c);
+    const uint16_t* from = w + row * cols;
+    const u32x4 v = c + 8u <= cols ? *(const u32x4_any*)(from + c) : load8(from, c, cols);
     uint32_t m = max_abs8(v);
     const uint32_t a = (uint32_t)__shfl_xor((int)m, 1, kWave);
     m = m > a ? m : a;
@@ -97,61 +98,64 @@ struct Fp4Args {
   const uint16_t* x;
   float* y;
   uint64_t rows;
-  uint32_t cols, batch, steps;
+  uint32_t cols, batch;
 };
 
-// 16 rows per block; its waves take every WPB-th step of 128 columns and add
-// their sums in LDS in wave order.  NT tiles of 16 input rows per wave; input
-// rows past the batch repeat the last one and are not stored.
-template <int NT, int WPB>
-__global__ __launch_bounds__(kWave * WPB) void k_fp4_gemv(Fp4Args a) {
-  __shared__ mfma_f32x4 part[WPB][NT][kWave];
-  const int lane = lane_id(), wave = wave_in_block();
-  const uint32_t r = (uint32_t)lane & 15u;
+// 16 rows per block, up to 16 input rows (QUAD: up to 4).  Each wave takes a run
+// of the steps, and their sums are added in LDS in wave order.  Input rows past
+// the batch repeat the last one and are not stored.
+template <bool QUAD, bool ANY, int U>
+__global__ __launch_bounds__(kWave * 16) void k_fp4_gemv(Fp4Args a) {
+  extern __shared__ mfma_f32x4 part[];  // [waves][kWave]
+  const uint32_t lane = (uint32_t)lane_id(), wave = (uint32_t)wave_in_block();
+  const uint32_t waves = blockDim.x / kWave;
   const uint64_t row0 = (uint64_t)blockIdx.x * kRowTile;
-  const uint64_t row = row0 + r < a.rows ? row0 + r : a.rows - 1u;
-  const uint32_t b0 = blockIdx.y * (kRowTile * NT);
-  const WeightRow w = weight_row<kFp4>(a.codes, a.scales, row, a.cols);
-  const uint16_t* x[NT];
-  mfma_f32x4 acc[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const uint32_t b = b0 + 16u * t + r;
-    x[t] = a.x + (uint64_t)(b < a.batch ? b : a.batch - 1u) * a.cols;
-    acc[t] = mfma_f32x4{0, 0, 0, 0};
-  }
+  const uint32_t b0 = blockIdx.y * kRowTile;
+  const uint32_t nb = a.batch - b0 < kRowTile ? a.batch - b0 : kRowTile;
+  const WeightTile<kFp4> w(a.codes, a.scales, row0, a.rows, a.cols);
+  const InputTile<QUAD, ANY> x(a.x + (uint64_t)b0 * a.cols, nb, a.cols,
+                               [&](uint32_t i) { return i < nb ? i : nb - 1u; });
+  Sums<QUAD> acc;
+  acc.clear();
   struct Slot {
-    WeightStep<kFp4> w;
-    u32x4 x[NT][4];
+    WeightStep w;
+    InputBlock<QUAD> x[4];
   };
-  const uint32_t n = a.steps > (uint32_t)wave ? (a.steps - 1u - (uint32_t)wave) / WPB + 1u : 0u;
-  step_ring<2, Slot>(
-      n,
-      [&](uint32_t q, Slot& s) {
-        const uint32_t step = q * WPB + (uint32_t)wave;
-        load_weights<kFp4>(w, step, a.cols, s.w);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) load_inputs<kFp4>(x[t], step, a.cols, s.x[t]);
-      },
-      [&](uint32_t, const Slot& s) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const u32x4 op = weight_operand<kFp4>(s.w, j);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) acc[t] = mfma16(op, s.x[t][j], acc[t]);
-        }
+  auto use = [&](Slot& s) __attribute__((always_inline)) {
+    quad_transpose(s.w.v);
+    each<4>([&](auto j) __attribute__((always_inline)) {
+      if constexpr (!QUAD) quad_transpose(s.x[j].v);
+      each<4>([&](auto k) __attribute__((always_inline)) {
+        acc.add(weight_operand<kFp4>(s.w, j, k), s.x[j], k);
       });
-#pragma unroll
-  for (int t = 0; t < NT; ++t) part[wave][t][lane] = acc[t];
+    });
+  };
+  const uint32_t whole = a.cols / kStepCols<kFp4>;
+  const uint32_t steps = (a.cols + kStepCols<kFp4> - 1u) / kStepCols<kFp4>;
+  const uint32_t s0 = wave * steps / waves, s1 = (wave + 1u) * steps / waves;
+  step_batches<U, Slot>(
+      (s1 < whole ? s1 : whole) - s0,
+      [&](uint32_t q, Slot& s) __attribute__((always_inline)) {
+        load_weights<kFp4, false>(w, s0 + q, s.w);
+        each<4>([&](auto j) __attribute__((always_inline)) {
+          load_inputs<kFp4, false>(x, s0 + q, j, s.x[j]);
+        });
+      },
+      use);
+  if (s1 > whole && s1 > s0) {  // the short last step
+    Slot s;
+    load_weights<kFp4, true>(w, whole, s.w);
+    each<4>([&](auto j) __attribute__((always_inline)) { load_inputs<kFp4, true>(x, whole, j, s.x[j]); });
+    use(s);
+  }
+  part[wave * kWave + lane] = acc.total();
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < NT * kWave; i += kWave * WPB) {
-    const uint32_t t = i / kWave, l = i % kWave;
-    mfma_f32x4 s = part[0][t][l];
-#pragma unroll
-    for (int v = 1; v < WPB; ++v) s += part[v][t][l];
-    const uint32_t b = b0 + 16u * t + (l & 15u);
-    const uint64_t y0 = row0 + 4u * (l >> 4);
-    if (b < a.batch) {
+  if (wave == 0) {
+    mfma_f32x4 s = part[lane];
+    for (uint32_t v = 1; v < waves; ++v) s += part[v * kWave + lane];
+    const uint32_t n = lane & 15u, b = b0 + (QUAD ? n >> 2 : n);
+    const uint64_t y0 = row0 + 4u * (lane >> 4);
+    if (b < a.batch && !(QUAD && (n & 3u))) {
 #pragma unroll
       for (uint32_t k = 0; k < 4; ++k)
         if (y0 + k < a.rows) a.y[(uint64_t)b * a.rows + y0 + k] = s[k];
@@ -168,6 +172,22 @@ int fp4_shape_ok(uint64_t rows, uint64_t cols) {
 }
 
 int launched() { return hipGetLastError() == hipSuccess ? WC_OK : WC_E_HIP; }
+
+// Waves per block: the blocks of a compute unit, all resident at once, share 16
+// (at up to 128 registers), and no wave is without a step.
+template <bool QUAD>
+void launch_rows(const Fp4Args& a, uint32_t row_blocks, uint32_t batch_blocks, hipStream_t s) {
+  const uint32_t steps = (a.cols + kStepCols<kFp4> - 1u) / kStepCols<kFp4>;
+  const uint32_t per_cu = (row_blocks + cu_count() - 1u) / cu_count();
+  uint32_t waves = per_cu < 16u ? 16u / per_cu : 1u;
+  waves = waves < steps ? waves : (steps ? steps : 1u);
+  const dim3 grid(row_blocks, batch_blocks);
+  const size_t lds = waves * kWave * sizeof(mfma_f32x4);
+  if (a.cols % 8u == 0)
+    k_fp4_gemv<QUAD, false, 1><<<grid, kWave * waves, lds, s>>>(a);
+  else
+    k_fp4_gemv<QUAD, true, 1><<<grid, kWave * waves, lds, s>>>(a);
+}
 
 uint32_t piece_blocks(uint64_t pieces) {
   const uint64_t b = (pieces + kBlockThreads - 1) / kBlockThreads;
@@ -212,15 +232,12 @@ extern "C" int wc_fp4_gemv(const uint8_t* d_codes, const uint8_t* d_scales, uint
     return WC_E_ARG;
   const uint64_t row_blocks = (rows + wc::kRowTile - 1) / wc::kRowTile;
   if (row_blocks >= (1ull << 31)) return WC_E_SIZE;
-  wc::Fp4Args a = {d_codes, d_scales, d_x, d_y, rows, (uint32_t)cols, batch,
-                   (uint32_t)((cols + wc::kStep - 1) / wc::kStep)};
+  wc::Fp4Args a = {d_codes, d_scales, d_x, d_y, rows, (uint32_t)cols, batch};
   hipStream_t s = (hipStream_t)stream;
-  const dim3 block(wc::kWave * 8);
-  if (batch <= 16)
-    wc::k_fp4_gemv<1, 8><<<dim3((uint32_t)row_blocks, 1), block, 0, s>>>(a);
-  else if (batch <= 32)
-    wc::k_fp4_gemv<2, 8><<<dim3((uint32_t)row_blocks, 1), block, 0, s>>>(a);
+  const uint32_t rb = (uint32_t)row_blocks;
+  if (batch <= 4)
+    wc::launch_rows<true>(a, rb, 1, s);
   else
-    wc::k_fp4_gemv<4, 8><<<dim3((uint32_t)row_blocks, (batch + 63u) / 64u), block, 0, s>>>(a);
+    wc::launch_rows<false>(a, rb, (batch + 15u) / 16u, s);
   return wc::launched();
 }

@@ -1,46 +1,67 @@
-// wc_skinny.h — products of weight rows with a few columns on the matrix
+// wc_skinny.h — products of weight rows with a few input rows on the matrix
 // cores, shared by the 4-bit GEMV (wc_fp4.hip) and the mixture-of-experts
 // layer (wc_moe.hip).
 //
-// One v_mfma_f32_16x16x32_bf16 multiplies 16 weight rows with up to 16 input
-// rows over 32 columns.  Lane l = r + 16 h gives 8 values of weight row r and
-// 8 values of input row r, and receives sums of input row r with weight rows
-// 4h .. 4h + 3.  The two operands only have to put the same column at the same
-// (h, element) place, so a wave's step of 128 columns (four of these) may take
-// its columns in the order in which they load best:
-//   4-bit weights  lane h owns columns 32h .. 32h + 31 of the step, one group:
-//                  16 bytes of codes and one scale, a single wide load
-//   BF16 weights   instance j owns columns 32j .. 32j + 31, lane h 8 of them,
-//                  so that every load covers 64 contiguous bytes of each row
+// One v_mfma_f32_16x16x32_bf16 multiplies 16 weight rows with 16 input rows
+// over 32 columns.  Lane r + 16 h gives 8 values of weight row r and 8 values of
+// input row r, and receives the sums of input row r with weight rows 4h .. 4h+3.
+// The two operands only have to put the same column at the same (h, element)
+// place, so any order of the columns will do.
+//
+// Loads in that lane order are slow: neighbouring lanes touch 16 different rows,
+// and the vector L1 then takes 64 cycles for a wave's 1 KB load (measured: 65,
+// bytes and dwords the same), where four neighbouring lanes on 64 contiguous
+// bytes take 17.  At 1 KB of 4-bit codes per 64 cycles and as much again for the
+// scales a compute unit gets 8 bytes per cycle, which bound the first form of
+// these kernels at about half of HBM's rate.  So lane 4b + j (+ 16 h) loads piece
+// j of row 4b + i in load i, for i = 0 .. 3, and the four registers are
+// transposed inside each quad of lanes by DPP: register j then holds piece j of
+// row r = 4b + i, as the MFMA wants it.
+//
+// Columns go by steps:
+//   4-bit weights  512 columns: piece (h, j) is the group of columns
+//                  128 h + 32 j .., one 16-byte load; four blocks j of four MFMAs
+//   BF16 weights   128 columns: piece (h, j) is columns 32 h + 8 j ..; one block
 #pragma once
+
+#include <type_traits>
 
 #include "wc_common.h"
 #include "wc_fp4.h"
 
 namespace wc {
 
-constexpr int kRowTile = 16;   // weight rows, and input rows, per MFMA
-constexpr int kStep = 128;     // columns per wave step
+constexpr uint32_t kRowTile = 16;  // weight rows, and input rows, per MFMA
 
-enum WeightKind { kBf16 = 0, kFp4 = 1 };
+enum WeightKind {
+  kBf16 = 0,
+  kFp4 = 1,
+  kBf16Any = 2,  // BF16 rows that start at any 2-byte address
+};
+template <int KIND>
+constexpr uint32_t kBlocks = KIND == kFp4 ? 4u : 1u;  // blocks of a step
+template <int KIND>
+constexpr uint32_t kStepCols = 128u * kBlocks<KIND>;
 
 typedef __bf16 mfma_bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 mfma_bf16x8 __attribute__((ext_vector_type(8)));
 typedef float mfma_f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
+typedef __amdgpu_buffer_rsrc_t buffer;
 
-__device__ inline mfma_f32x4 mfma16(u32x4 a, u32x4 b, mfma_f32x4 c) {
+__device__ __forceinline__ mfma_f32x4 mfma16(u32x4 a, u32x4 b, mfma_f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(mfma_bf16x8, a),
                                                  __builtin_bit_cast(mfma_bf16x8, b), c, 0, 0, 0);
 }
 
 // The scale 2^(e - 127) as the conversion instructions take it: they use the
 // exponent field alone, so e = 0 is 2^-127 and e = 255 gives NaN.
-__device__ inline float fp4_scale(uint32_t e) { return __uint_as_float(e << 23); }
+__device__ __forceinline__ float fp4_scale(uint32_t e) { return __uint_as_float(e << 23); }
 
 // 8 codes (low nibble first) times their scale, as 8 BF16 values: four
 // conversions, exact within BF16's range.
-__device__ inline u32x4 fp4_expand(uint32_t codes, float scale) {
+__device__ __forceinline__ u32x4 fp4_expand(uint32_t codes, float scale) {
   u32x4 w;
   w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0));
   w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1));
@@ -49,114 +70,268 @@ __device__ inline u32x4 fp4_expand(uint32_t codes, float scale) {
   return w;
 }
 
-__device__ inline uint16_t bf16_of(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+__device__ __forceinline__ uint16_t bf16_of(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
-// 8 BF16 values at p, of which the first `left` exist (the rest are 0, and
-// are not read).  Rows of an odd length start at any 2-byte address.
-__device__ inline u32x4 load8(const uint16_t* __restrict__ p, int left) {
-  if (left >= 8) return *(const u32x4_any*)p;
-  u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 7; ++i)
-    if (i < left) v[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
-  return v;
+// f(0), .., f(N - 1) with constant arguments: registers indexed by them stay
+// registers.
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  if constexpr (N > 0) {
+    each<N - 1>(f);
+    f(std::integral_constant<int, N - 1>{});
+  }
 }
 
-// A lane's view of a weight row and of an input row.
-struct WeightRow {
-  const uint8_t* data;    // 4-bit: the lane's first group; BF16: the lane's first value
-  const uint8_t* scales;  // 4-bit: the lane's first scale
+// ---- loads -------------------------------------------------------------------
+
+// Bytes [0, n) from p on (wave-uniform).  What a load asks for past them reads as
+// 0 and touches no memory; kNowhere is such an offset for every buffer here.
+__device__ __forceinline__ buffer buffer_of(const void* p, uint32_t n) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)n, 0x00027000);
+}
+constexpr uint32_t kNowhere = 0xFFFFFF00u;
+__device__ __forceinline__ u32x4 load16(buffer b, uint32_t lane_off, uint32_t off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)lane_off, (int)off, 0));
+}
+
+// Values c .. c + 7 of a row of `cols` BF16 values (cols >= 1); what lies past
+// the row is 0.  Rows of an odd length start at any 2-byte address.  A piece that
+// the row's end cuts is taken from the row's last 8 values and shifted down, so
+// that every piece is one load within the row.
+__device__ inline u32x4 load8(const uint16_t* __restrict__ row, uint32_t c, uint32_t cols) {
+  if (cols < 8u) {  // the same for all lanes
+    uint32_t e[8];
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) e[i] = row[i < cols ? i : cols - 1u];
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) e[i] = c + i < cols ? e[i] : 0u;  // c is a multiple of 8
+    return u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+  }
+  const uint32_t from = c < cols - 8u ? c : cols - 8u, off = c - from;
+  const u32x4 v = *(const u32x4_any*)(row + from);
+  uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+  if (off >= 4u) {
+    lo = hi;
+    hi = 0;
+  }
+  const uint32_t sh = 16u * (off & 3u);
+  lo = lo >> sh | (hi << 1) << (63u - sh);
+  hi >>= sh;
+  if (off >= 8u) lo = hi = 0;
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
+// a of the lanes with `up` set and b of the others change places across PERM.
+template <int PERM>
+__device__ __forceinline__ void quad_swap(u32x4& a, u32x4& b, bool up) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t x = a[k], y = b[k];
+    const uint32_t xs = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, PERM, 0xF, 0xF, true);
+    const uint32_t ys = (uint32_t)__builtin_amdgcn_mov_dpp((int)y, PERM, 0xF, 0xF, true);
+    a[k] = up ? ys : x;
+    b[k] = up ? y : xs;
+  }
+}
+
+// v[j] of lane 4b + i <- v[i] of lane 4b + j.
+__device__ __forceinline__ void quad_transpose(u32x4 v[4]) {
+  const bool odd = lane_id() & 1, high = lane_id() & 2;
+  quad_swap<0xB1>(v[0], v[1], odd);  // lanes 1 0 3 2
+  quad_swap<0xB1>(v[2], v[3], odd);
+  quad_swap<0x4E>(v[0], v[2], high);  // lanes 2 3 0 1
+  quad_swap<0x4E>(v[1], v[3], high);
+}
+
+// ---- weights -----------------------------------------------------------------
+
+// 16 weight rows, row0 .. row0 + 15 of `rows` (those past the end repeat the last
+// one, and their sums are not used), seen by one lane.
+template <int KIND>
+struct WeightTile {
+  const uint8_t* data;  // of row0; wave-uniform
+  uint32_t bytes;
+  uint32_t off[4];        // the lane's piece of row 4b + i
+  const uint8_t* scales;  // kFp4: of the lane's MFMA row r, from group 4 h on
+  uint32_t cols;
+
+  __device__ __forceinline__ WeightTile(const void* d, const uint8_t* s, uint64_t row0, uint64_t rows,
+                                        uint32_t c)
+      : cols(c) {
+    const uint32_t lane = (uint32_t)lane_id(), r = lane & 15u, h = lane >> 4;
+    const uint32_t n = rows - row0 < 16u ? (uint32_t)(rows - row0) : 16u;
+    const uint32_t groups = (uint32_t)WC_FP4_GROUPS(c);
+    const uint32_t row_bytes = KIND == kFp4 ? groups * 16u : c * 2u;
+    data = (const uint8_t*)d + row0 * row_bytes;
+    bytes = n * row_bytes;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+      const uint32_t q = (r & ~3u) + i;
+      off[i] = (q < n ? q : n - 1u) * row_bytes + 64u * h + 16u * (r & 3u);
+    }
+    if constexpr (KIND == kFp4) scales = s + (row0 + (r < n ? r : n - 1u)) * groups + 4u * h;
+  }
 };
 
-// Row `row` of an array of rows of `cols` columns.
-template <int KIND>
-__device__ inline WeightRow weight_row(const void* data, const uint8_t* scales, uint64_t row,
-                                       uint32_t cols) {
-  const uint32_t h = (uint32_t)lane_id() >> 4;
-  WeightRow w;
-  if constexpr (KIND == kFp4) {
-    const uint64_t groups = WC_FP4_GROUPS(cols);
-    w.data = (const uint8_t*)data + (row * groups + h) * 16u;
-    w.scales = scales + row * groups + h;
-  } else {
-    w.data = (const uint8_t*)((const uint16_t*)data + row * cols + 8u * h);
-    w.scales = nullptr;
-  }
-  return w;
-}
-
-// A lane's weights of one step.
-template <int KIND>
+// A lane's weights of one step; kFp4: with the scales of its four groups.
 struct WeightStep {
-  u32x4 v[KIND == kFp4 ? 1 : 4];
+  u32x4 v[4];
   uint32_t e;
 };
 
-template <int KIND>
-__device__ inline void load_weights(const WeightRow& w, uint32_t step, uint32_t cols,
-                                    WeightStep<KIND>& s) {
-  const bool whole = (step + 1) * kStep <= cols;  // the same for all lanes
-  const uint32_t h = (uint32_t)lane_id() >> 4;
+// TAIL: the row's last step, of which some columns do not exist: they read as 0.
+template <int KIND, bool TAIL>
+__device__ __forceinline__ void load_weights(const WeightTile<KIND>& w, uint32_t step, WeightStep& s) {
+  const uint32_t lane = (uint32_t)lane_id(), h = lane >> 4, j = lane & 3u;
   if constexpr (KIND == kFp4) {
-    const bool in = whole || step * kStep + 32u * h < cols;  // padding nibbles are 0
-    if (in) {
-      s.v[0] = __builtin_nontemporal_load((const u32x4*)(w.data + (size_t)step * 64u));
-      s.e = w.scales[step * 4u];
+    const buffer b = buffer_of(w.data, w.bytes);
+    const uint32_t groups = (uint32_t)WC_FP4_GROUPS(w.cols);
+    const bool in = !TAIL || step * 16u + 4u * h + j < groups;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s.v[i] = load16(b, in ? w.off[i] : kNowhere, step * 256u);
+    if constexpr (TAIL) {
+      s.e = 0;
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k)
+        if (step * 16u + 4u * h + k < groups) s.e |= (uint32_t)w.scales[step * 16u + k] << (8u * k);
     } else {
-      s.v[0] = u32x4{0, 0, 0, 0};
-      s.e = 127;
+      s.e = *(const u32_any*)(w.scales + step * 16u);
     }
+  } else if constexpr (KIND == kBf16) {
+    const buffer b = buffer_of(w.data, w.bytes);
+    const bool in = !TAIL || step * 128u + 32u * h + 8u * j < w.cols;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s.v[i] = load16(b, in ? w.off[i] : kNowhere, step * 256u);
   } else {
-    const uint16_t* p = (const uint16_t*)w.data + (size_t)step * kStep;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int left = (int)cols - (int)(step * kStep + 32u * j + 8u * h);
-      s.v[j] = whole ? *(const u32x4_any*)(p + 32 * j) : load8(p + 32 * j, left);
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t* p = w.data + w.off[i];
+      if constexpr (TAIL)
+        s.v[i] = load8((const uint16_t*)(p - 64u * h - 16u * j), step * 128u + 32u * h + 8u * j, w.cols);
+      else
+        s.v[i] = *(const u32x4_any*)(p + (size_t)step * 256u);
     }
   }
 }
 
-// A lane's values of one input row in one step, in the weights' column order;
-// x points at the row.
+// Operand k (0 .. 3) of block j, after quad_transpose(s.v).
 template <int KIND>
-__device__ inline void load_inputs(const uint16_t* __restrict__ x, uint32_t step, uint32_t cols,
-                                   u32x4 v[4]) {
-  const bool whole = (step + 1) * kStep <= cols;
+__device__ __forceinline__ u32x4 weight_operand(const WeightStep& s, int j, int k) {
+  if constexpr (KIND == kFp4) {
+    const uint32_t e = j == 0 ? s.e << 23 : j == 1 ? s.e << 15 : j == 2 ? s.e << 7 : s.e >> 1;
+    return fp4_expand(s.v[j][k], __uint_as_float(e & 0x7F800000u));
+  } else {
+    return s.v[k];
+  }
+}
+
+// n steps, U at a time: the loads of U steps go out together, then the steps are
+// used; the other waves of the compute unit have theirs in flight meanwhile.
+// Loading a step ahead of its use measured slower here: past the end such a
+// pipeline either loads for nothing (each load costs its address cycles) or
+// branches, and then every wait is for all loads.
+template <int U, typename Slot, typename Load, typename Use>
+__device__ __forceinline__ void step_batch(uint32_t q, Load&& load, Use&& use) {
+  Slot s[U];
+  each<U>([&](auto i) __attribute__((always_inline)) { load(q + i, s[i]); });
+  __builtin_amdgcn_sched_barrier(0);  // no load moves down among the uses
+  each<U>([&](auto i) __attribute__((always_inline)) { use(s[i]); });
+}
+template <int U, typename Slot, typename Load, typename Use>
+__device__ __forceinline__ void step_batches(uint32_t n, Load&& load, Use&& use) {
+  uint32_t q = 0;
+  for (; q + U <= n; q += U) step_batch<U, Slot>(q, load, use);
+  const uint32_t left = n - q;
+  each<U>([&](auto i) __attribute__((always_inline)) {
+    if constexpr (i > 0)
+      if (left == (uint32_t)i) step_batch<i, Slot>(q, load, use);
+  });
+}
+
+// ---- inputs ------------------------------------------------------------------
+
+// First column of a lane's block j in a step.
+template <int KIND>
+__device__ __forceinline__ uint32_t input_col(int j) {
   const uint32_t h = (uint32_t)lane_id() >> 4;
+  return KIND == kFp4 ? 128u * h + 32u * (uint32_t)j : 32u * h;
+}
+
+// Up to 16 input rows.
+//   full   loads i = 0 .. 3 take piece lane & 3 of input row 4b + i, and after
+//          quad_transpose register k is operand k, with input row r in column r
+//   QUAD   up to four input rows: one load, lane 4 b + k has piece k of row b.
+//          Operand k multiplies it whole, into sums of its own, of which column
+//          4 b + k is what it should be (Sums below): no transposition
+// ANY: rows that start at any 2-byte address.
+template <bool QUAD, bool ANY>
+struct InputTile {
+  static constexpr int kLoads = QUAD ? 1 : 4;
+  const uint16_t* base;  // wave-uniform
+  uint32_t bytes, cols;
+  uint32_t row[kLoads];  // the input rows that the lane loads
+
+  // The first n of the rows at x, of c columns each; row_of(i) is the input row
+  // for column i of the product.
+  template <typename F>
+  __device__ __forceinline__ InputTile(const uint16_t* x, uint32_t n, uint32_t c, F&& row_of)
+      : base(x), bytes(n * c * 2u), cols(c) {
+    const uint32_t r = (uint32_t)lane_id() & 15u;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t c = step * kStep + (KIND == kFp4 ? 32u * h + 8u * j : 32u * j + 8u * h);
-    v[j] = whole ? *(const u32x4_any*)(x + c) : load8(x + c, (int)cols - (int)c);
+    for (int i = 0; i < kLoads; ++i) row[i] = row_of(QUAD ? r >> 2 : (r & ~3u) + (uint32_t)i);
   }
-}
+};
 
-// Instance j's weight operand.
-template <int KIND>
-__device__ inline u32x4 weight_operand(const WeightStep<KIND>& s, int j) {
-  if constexpr (KIND == kFp4)
-    return fp4_expand(s.v[0][j], fp4_scale(s.e));
-  else
-    return s.v[j];
-}
+template <bool QUAD>
+struct InputBlock {
+  u32x4 v[QUAD ? 1 : 4];
+};
 
-// Software pipeline over n steps with D slots: step q + D - 1 is loaded just
-// before step q is used.  Past the end the last step is loaded again, so the
-// loads in flight are the same on every path.
-template <int D, typename Slot, typename Load, typename Use>
-__device__ inline void step_ring(uint32_t n, Load&& load, Use&& use) {
-  if (n == 0) return;
-  Slot s[D];
+template <int KIND, bool TAIL, bool QUAD, bool ANY>
+__device__ __forceinline__ void load_inputs(const InputTile<QUAD, ANY>& x, uint32_t step, int j,
+                                            InputBlock<QUAD>& s) {
+  const uint32_t c = input_col<KIND>(j) + 8u * ((uint32_t)lane_id() & 3u);
+  const uint32_t at = step * kStepCols<KIND> + c;
 #pragma unroll
-  for (int i = 0; i < D - 1; ++i) load((uint32_t)i < n ? (uint32_t)i : n - 1u, s[i]);
-  for (uint32_t q = 0; q < n; q += D) {
-#pragma unroll
-    for (int i = 0; i < D; ++i) {
-      const uint32_t next = q + i + D - 1;
-      load(next < n ? next : n - 1u, s[(i + D - 1) % D]);
-      if (q + i >= n) return;
-      use(q + i, s[i]);
+  for (int i = 0; i < (QUAD ? 1 : 4); ++i) {
+    if constexpr (ANY) {
+      const uint16_t* row = x.base + (uint64_t)x.row[i] * x.cols;
+      s.v[i] = TAIL ? load8(row, at, x.cols) : *(const u32x4_any*)(row + at);
+    } else {
+      const bool in = !TAIL || at < x.cols;
+      s.v[i] = load16(buffer_of(x.base, x.bytes), in ? (x.row[i] * x.cols + c) * 2u : kNowhere,
+                      step * kStepCols<KIND> * 2u);
     }
   }
 }
+
+template <bool QUAD>
+struct Sums {
+  mfma_f32x4 v[QUAD ? 4 : 1];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < (QUAD ? 4 : 1); ++j) v[j] = mfma_f32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ void add(u32x4 weights, const InputBlock<QUAD>& x, int k) {
+    v[QUAD ? k : 0] = mfma16(weights, x.v[QUAD ? 0 : k], v[QUAD ? k : 0]);
+  }
+  // Sums of input row b in every column of quad b (full: of row n in column n).
+  __device__ __forceinline__ mfma_f32x4 total() const {
+    if constexpr (!QUAD) {
+      return v[0];
+    } else {
+      const uint32_t j = (uint32_t)lane_id() & 3u;
+      mfma_f32x4 t;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float s = j == 0 ? v[0][k] : j == 1 ? v[1][k] : j == 2 ? v[2][k] : v[3][k];
+        s += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(s), 0xB1, 0xF, 0xF, true));
+        s += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(s), 0x4E, 0xF, 0xF, true));
+        t[k] = s;
+      }
+      return t;
+    }
+  }
+};
 
 }  // namespace wc

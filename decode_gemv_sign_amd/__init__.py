@@ -22,6 +22,7 @@ without a built libwc.so raises ImportError.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -157,14 +158,17 @@ def _check(st: int, what: str):
         raise WCError(st, what)
 
 
-def _stream(stream=None) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(stream=None) -> int:
+    """The hipStream_t to use: the current one's handle, read without building
+    a torch Stream (0.2 against 3 us, a fifth of a small call)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _on_device(t: torch.Tensor) -> bool:
     """True for a tensor in GPU memory (the library takes device pointers only)."""
-    return t.device.type == "cuda"
+    return t.is_cuda
 
 
 def _bits16(t: torch.Tensor, what: str) -> torch.Tensor:
@@ -192,9 +196,11 @@ def _bytes(t: torch.Tensor, what: str, need: int) -> torch.Tensor:
 
 
 def _same_device(what: str, *ts: torch.Tensor):
-    devs = {t.device for t in ts}
-    if len(devs) > 1:
-        raise ValueError(f"{what}: tensors on different devices {sorted(map(str, devs))}")
+    first = ts[0].get_device()
+    for t in ts:
+        if t.get_device() != first:
+            devs = sorted({str(t.device) for t in ts})
+            raise ValueError(f"{what}: tensors on different devices {devs}")
 
 
 def _batch_of(x: torch.Tensor, cols: int, what: str = "x") -> int:
@@ -227,8 +233,8 @@ def _gemv_out(out: torch.Tensor, batch: int, rows: int, what: str = "out") -> to
     return out
 
 
-def _ptr(t: torch.Tensor | None) -> ctypes.c_void_p:
-    return ctypes.c_void_p(t.data_ptr() if t is not None and t.numel() else 0)
+def _ptr(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
 
 
 def workspace_bytes(n: int) -> int:
@@ -468,6 +474,13 @@ class Fp4(NamedTuple):
 def _fp4(q: Fp4, what: str):
     """(leading dims, rows, cols) of a checked Fp4."""
     codes, scales, cols = q
+    shape, groups = scales.shape, (cols + FP4_GROUP - 1) // FP4_GROUP
+    if (len(shape) in (2, 3) and shape[-1] == groups and cols >= 0
+            and codes.shape == (*shape[:-1], 16 * groups)
+            and codes.dtype is torch.uint8 and scales.dtype is torch.uint8
+            and codes.is_contiguous() and scales.is_contiguous()
+            and _on_device(codes) and _on_device(scales)):
+        return shape[:-2], shape[-2], cols
     for t, name in ((codes, "codes"), (scales, "scales")):
         if not _on_device(t):
             raise ValueError(f"{what}.{name} must be a device tensor")
@@ -475,21 +488,14 @@ def _fp4(q: Fp4, what: str):
             raise TypeError(f"{what}.{name} must be a uint8 tensor")
         if not t.is_contiguous():
             raise ValueError(f"{what}.{name} must be contiguous")
-    cols = int(cols)
-    shape = tuple(scales.shape)
-    if cols < 0 or len(shape) not in (2, 3) or shape[-1] != (cols + FP4_GROUP - 1) // FP4_GROUP:
-        raise ValueError(f"{what}.scales has shape {shape}, expected [.., rows, "
-                         f"{(cols + FP4_GROUP - 1) // FP4_GROUP}] for {cols} columns")
-    if tuple(codes.shape) != shape[:-1] + (16 * shape[-1],):
-        raise ValueError(f"{what}.codes has shape {tuple(codes.shape)}, expected "
-                         f"{shape[:-1] + (16 * shape[-1],)}")
-    return shape[:-2], shape[-2], cols
+    raise ValueError(f"{what}: codes {tuple(codes.shape)} and scales {tuple(shape)} are not "
+                     f"[.., rows, {16 * groups}] and [.., rows, {groups}] of {cols} columns")
 
 
 def _used_on(stream, *tensors):
     """Memory allocated here on the current stream and used on another one is
     not handed out again before that one is done with it."""
-    if stream is not None and stream != torch.cuda.current_stream():
+    if stream is not None and stream.cuda_stream != _stream():
         for t in tensors:
             t.record_stream(stream)
 
@@ -561,6 +567,7 @@ def _moe_shape(tokens, hidden, inter, experts, top_k, scoring, renorm, scale) ->
                     scale)
 
 
+@functools.lru_cache(maxsize=256)
 def moe_workspace_bytes(tokens: int, hidden: int, inter: int, experts: int, top_k: int) -> int:
     """wc_moe_workspace_bytes: device scratch of one moe call of that shape."""
     need = _lib.wc_moe_workspace_bytes(
@@ -613,8 +620,7 @@ def moe(x: torch.Tensor, router: torch.Tensor, gate_up, down, top_k: int, *, sco
             raise TypeError("bias must be float32")
         if tuple(bias.shape) != (experts,) or not bias.is_contiguous():
             raise ValueError(f"bias must be a contiguous [{experts}], got {tuple(bias.shape)}")
-    shape = _moe_shape(tokens, hidden, inter, experts, top_k, scoring, renorm, scale)
-    need = _lib.wc_moe_workspace_bytes(ctypes.byref(shape))
+    need = moe_workspace_bytes(tokens, hidden, inter, experts, top_k)
     if work is None:
         work = torch.empty(need, dtype=torch.uint8, device=x.device)
         _used_on(stream, work)
@@ -628,6 +634,7 @@ def moe(x: torch.Tensor, router: torch.Tensor, gate_up, down, top_k: int, *, sco
     weights = torch.empty((tokens, top_k), dtype=torch.float32, device=x.device)
     _used_on(stream, ids, weights)
     _same_device("moe", x, router, work, out, *tgu, *tdn, *(() if bias is None else (bias,)))
+    shape = _moe_shape(tokens, hidden, inter, experts, top_k, scoring, renorm, scale)
     _check(_lib.wc_moe(ctypes.byref(shape), _ptr(x), _ptr(router), _ptr(bias), ctypes.byref(cgu),
                        ctypes.byref(cdn), _ptr(out), _ptr(ids), _ptr(weights), _ptr(work),
                        work.numel(), _stream(stream)), "wc_moe")

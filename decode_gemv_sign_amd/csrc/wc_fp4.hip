@@ -163,6 +163,107 @@ __global__ __launch_bounds__(kWave * 16) void k_fp4_gemv(Fp4Args a) {
   }
 }
 
+// Batches above 16: each wave has 32 rows, and every input operand feeds two
+// products.  Block = RT row parts x KG column parts; the RT waves of a column part
+// share the inputs of one block of 128 columns (wc_skinny.h), NT tiles of 16
+// input rows, in LDS, brought there a block ahead by global->LDS loads: load i of
+// a tile takes, lane 4b + k (+ 16 h), piece k of input row 4b + i, so quads read
+// 64 contiguous bytes; 16 bytes of padding after every load put the 16 pieces
+// that one operand read takes at a time in different banks.
+constexpr uint32_t kWideLoad = 1024u + 16u;
+template <int NT, int RT, int KG>
+__global__ __launch_bounds__(kWave * RT * KG) void k_fp4_wide(Fp4Args a) {
+  constexpr uint32_t kBuf = NT * 4u * kWideLoad;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // [KG][2][kBuf], then the sums
+  const uint32_t lane = (uint32_t)lane_id(), wave = (uint32_t)wave_in_block();
+  const uint32_t rt = wave % RT, kg = wave / RT;
+  const uint32_t r = lane & 15u, h = lane >> 4;
+  const uint64_t row0 = ((uint64_t)blockIdx.x * RT + rt) * 32u;
+  const uint32_t b0 = blockIdx.y * (kRowTile * NT);
+  // a row part past the end works on the last rows and stores nothing
+  const uint64_t at = row0 < a.rows ? row0 : a.rows - 1u;
+  const WeightTile<kFp4> w0(a.codes, a.scales, at, a.rows, a.cols);
+  const WeightTile<kFp4> w1(a.codes, a.scales, at + 16u < a.rows ? at + 16u : at, a.rows, a.cols);
+  uint8_t* const mine = lds + kg * (2u * kBuf);
+  const uint32_t steps = (a.cols + kStepCols<kFp4> - 1u) / kStepCols<kFp4>;
+  const uint32_t whole = a.cols / kStepCols<kFp4>;
+  const uint32_t s0 = kg * steps / KG, s1 = (kg + 1u) * steps / KG;
+  const uint32_t turns = (steps + KG - 1u) / KG * 4u;  // blocks per column part, at most
+  // this wave's share of a block's input loads
+  auto stage = [&](uint32_t turn, uint32_t buf) __attribute__((always_inline)) {
+    const uint32_t s = s0 + turn / 4u, j = turn & 3u;
+    if (s >= s1) return;
+    const uint32_t c = s * kStepCols<kFp4> + 128u * h + 32u * j + 8u * (lane & 3u);
+#pragma unroll
+    for (uint32_t q = 0; q < NT * 4u / RT; ++q) {
+      const uint32_t load = q * RT + rt;  // tile load / 4, rows 4b + load % 4
+      const uint32_t b = b0 + (load / 4u) * 16u + (r & ~3u) + load % 4u;
+      const uint16_t* from = a.x + (uint64_t)(b < a.batch ? b : a.batch - 1u) * a.cols + c;
+      uint8_t* to = mine + buf * kBuf + load * kWideLoad;
+      if (s < whole)
+        lds_dma16_keep(from, (uint32_t*)to);
+      else  // cols is a multiple of 8: a piece is in or out
+        *(u32x4*)(to + 16u * lane) = c < a.cols ? *(const u32x4*)from : u32x4{0, 0, 0, 0};
+    }
+  };
+  mfma_f32x4 acc[2][NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[0][t] = acc[1][t] = mfma_f32x4{0, 0, 0, 0};
+  WeightStep v0, v1;
+  stage(0, 0);
+  for (uint32_t turn4 = 0; turn4 < turns; turn4 += 4u) {
+    const uint32_t s = s0 + turn4 / 4u;
+    if (s < whole) {
+      load_weights<kFp4, false>(w0, s, v0);
+      load_weights<kFp4, false>(w1, s, v1);
+    } else if (s < s1) {
+      load_weights<kFp4, true>(w0, s, v0);
+      load_weights<kFp4, true>(w1, s, v1);
+    }
+    quad_transpose(v0.v);
+    quad_transpose(v1.v);
+    each<4>([&](auto j) __attribute__((always_inline)) {
+      wait_vm<0>();
+      __syncthreads();  // block j is in, and the other buffer has been read
+      stage(turn4 + j + 1u, (j + 1u) & 1u);
+      if (s < s1) {
+        const uint8_t* in = mine + (j & 1u) * kBuf + (r & 3u) * kWideLoad + (4u * (r >> 2) + 16u * h) * 16u;
+        each<4>([&](auto k) __attribute__((always_inline)) {
+          const u32x4 o0 = weight_operand<kFp4>(v0, j, k), o1 = weight_operand<kFp4>(v1, j, k);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const u32x4 x = *(const u32x4*)(in + t * 4u * kWideLoad + 16u * k);
+            acc[0][t] = mfma16(o0, x, acc[0][t]);
+            acc[1][t] = mfma16(o1, x, acc[1][t]);
+          }
+        });
+      }
+    });
+  }
+  // the column parts' sums, in order
+  __syncthreads();
+  mfma_f32x4* const part = (mfma_f32x4*)lds;  // [KG][RT][2][NT][kWave]
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) part[((wave * 2u + m) * NT + t) * kWave + lane] = acc[m][t];
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < RT * 2u * NT * kWave; i += kWave * RT * KG) {
+    mfma_f32x4 s = part[i];
+#pragma unroll
+    for (uint32_t v = 1; v < KG; ++v) s += part[v * (RT * 2u * NT * kWave) + i];
+    // kg 0's waves are 0 .. RT - 1, so i is (rt, m, t, lane)
+    const uint32_t l = i % kWave, t = i / kWave % NT, m = i / (kWave * NT) % 2u, q = i / (kWave * NT * 2u);
+    const uint32_t b = b0 + 16u * t + (l & 15u);
+    const uint64_t y0 = ((uint64_t)blockIdx.x * RT + q) * 32u + 16u * m + 4u * (l >> 4);
+    if (b < a.batch) {
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k)
+        if (y0 + k < a.rows) a.y[(uint64_t)b * a.rows + y0 + k] = s[k];
+    }
+  }
+}
+
 namespace {
 
 int fp4_shape_ok(uint64_t rows, uint64_t cols) {
@@ -187,6 +288,14 @@ void launch_rows(const Fp4Args& a, uint32_t row_blocks, uint32_t batch_blocks, h
     k_fp4_gemv<QUAD, false, 1><<<grid, kWave * waves, lds, s>>>(a);
   else
     k_fp4_gemv<QUAD, true, 1><<<grid, kWave * waves, lds, s>>>(a);
+}
+
+template <int NT, int RT, int KG>
+void launch_wide(const Fp4Args& a, hipStream_t s) {
+  const uint32_t row_blocks = (uint32_t)((a.rows + RT * 32u - 1u) / (RT * 32u));
+  const size_t in = (size_t)KG * 2u * NT * 4u * kWideLoad, sums = (size_t)KG * RT * 2u * NT * 1024u;
+  k_fp4_wide<NT, RT, KG><<<dim3(row_blocks, (a.batch + 16u * NT - 1u) / (16u * NT)), kWave * RT * KG,
+                           in > sums ? in : sums, s>>>(a);
 }
 
 uint32_t piece_blocks(uint64_t pieces) {
@@ -237,7 +346,11 @@ extern "C" int wc_fp4_gemv(const uint8_t* d_codes, const uint8_t* d_scales, uint
   const uint32_t rb = (uint32_t)row_blocks;
   if (batch <= 4)
     wc::launch_rows<true>(a, rb, 1, s);
-  else
+  else if (batch <= 16 || cols % 8u)
     wc::launch_rows<false>(a, rb, (batch + 15u) / 16u, s);
+  else if (batch <= 32)
+    wc::launch_wide<2, 1, 8>(a, s);
+  else
+    wc::launch_wide<4, 2, 4>(a, s);
   return wc::launched();
 }

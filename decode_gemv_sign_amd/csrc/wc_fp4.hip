@@ -163,99 +163,103 @@ __global__ __launch_bounds__(kWave * 16) void k_fp4_gemv(Fp4Args a) {
   }
 }
 
-// Batches above 16: each wave has 32 rows, and every input operand feeds two
-// products.  Block = RT row parts x KG column parts; the RT waves of a column part
-// share the inputs of one block of 128 columns (wc_skinny.h), NT tiles of 16
-// input rows, in LDS, brought there a block ahead by global->LDS loads: load i of
-// a tile takes, lane 4b + k (+ 16 h), piece k of input row 4b + i, so quads read
-// 64 contiguous bytes; 16 bytes of padding after every load put the 16 pieces
-// that one operand read takes at a time in different banks.
+// Larger batches: MT x 16 weight rows by NT x 16 input rows per block, each of
+// its waves a run of the steps.  The inputs of one block of 128 columns
+// (wc_skinny.h) come to the wave's own part of LDS a block ahead, by global->LDS
+// loads: load i of a tile takes, lane 4b + k (+ 16 h), piece k of input row 4b + i,
+// so quads read 64 contiguous bytes, and the operand reads do the transposition;
+// 16 bytes of padding after every load put the pieces that one operand read takes
+// at a time in different banks.  Nothing is shared between waves until the end,
+// so there is no barrier for their loads to wait at.
 constexpr uint32_t kWideLoad = 1024u + 16u;
-template <int NT, int RT, int KG>
-__global__ __launch_bounds__(kWave * RT * KG) void k_fp4_wide(Fp4Args a) {
+template <int MT, int NT, int KG>
+__global__ __launch_bounds__(kWave * KG) void k_fp4_wide(Fp4Args a) {
   constexpr uint32_t kBuf = NT * 4u * kWideLoad;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // [KG][2][kBuf], then the sums
-  const uint32_t lane = (uint32_t)lane_id(), wave = (uint32_t)wave_in_block();
-  const uint32_t rt = wave % RT, kg = wave / RT;
+  const uint32_t lane = (uint32_t)lane_id(), kg = (uint32_t)wave_in_block();
   const uint32_t r = lane & 15u, h = lane >> 4;
-  const uint64_t row0 = ((uint64_t)blockIdx.x * RT + rt) * 32u;
+  const uint64_t row0 = (uint64_t)blockIdx.x * (kRowTile * MT);
   const uint32_t b0 = blockIdx.y * (kRowTile * NT);
-  // a row part past the end works on the last rows and stores nothing
-  const uint64_t at = row0 < a.rows ? row0 : a.rows - 1u;
-  const WeightTile<kFp4> w0(a.codes, a.scales, at, a.rows, a.cols);
-  const WeightTile<kFp4> w1(a.codes, a.scales, at + 16u < a.rows ? at + 16u : at, a.rows, a.cols);
   uint8_t* const mine = lds + kg * (2u * kBuf);
   const uint32_t steps = (a.cols + kStepCols<kFp4> - 1u) / kStepCols<kFp4>;
   const uint32_t whole = a.cols / kStepCols<kFp4>;
   const uint32_t s0 = kg * steps / KG, s1 = (kg + 1u) * steps / KG;
-  const uint32_t turns = (steps + KG - 1u) / KG * 4u;  // blocks per column part, at most
-  // this wave's share of a block's input loads
-  auto stage = [&](uint32_t turn, uint32_t buf) __attribute__((always_inline)) {
-    const uint32_t s = s0 + turn / 4u, j = turn & 3u;
-    if (s >= s1) return;
+  // the lane's input rows
+  const uint16_t* x[NT * 4];
+  each<NT * 4>([&](auto i) __attribute__((always_inline)) {
+    const uint32_t b = b0 + (i / 4u) * 16u + (r & ~3u) + i % 4u;
+    x[i] = a.x + (uint64_t)(b < a.batch ? b : a.batch - 1u) * a.cols;
+  });
+  auto stage = [&](uint32_t s, auto j, uint32_t buf) __attribute__((always_inline)) {
     const uint32_t c = s * kStepCols<kFp4> + 128u * h + 32u * j + 8u * (lane & 3u);
-#pragma unroll
-    for (uint32_t q = 0; q < NT * 4u / RT; ++q) {
-      const uint32_t load = q * RT + rt;  // tile load / 4, rows 4b + load % 4
-      const uint32_t b = b0 + (load / 4u) * 16u + (r & ~3u) + load % 4u;
-      const uint16_t* from = a.x + (uint64_t)(b < a.batch ? b : a.batch - 1u) * a.cols + c;
-      uint8_t* to = mine + buf * kBuf + load * kWideLoad;
-      if (s < whole)
-        lds_dma16_keep(from, (uint32_t*)to);
-      else  // cols is a multiple of 8: a piece is in or out
-        *(u32x4*)(to + 16u * lane) = c < a.cols ? *(const u32x4*)from : u32x4{0, 0, 0, 0};
+    uint8_t* const to = mine + buf * kBuf;
+    if (s < whole) {
+      each<NT * 4>([&](auto i) __attribute__((always_inline)) {
+        lds_dma16_keep(x[i] + c, (uint32_t*)(to + i * kWideLoad));
+      });
+    } else {  // cols is a multiple of 8: a piece is in or out
+      each<NT * 4>([&](auto i) __attribute__((always_inline)) {
+        *(u32x4*)(to + i * kWideLoad + 16u * lane) = c < a.cols ? *(const u32x4*)(x[i] + c) : u32x4{0, 0, 0, 0};
+      });
     }
   };
-  mfma_f32x4 acc[2][NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) acc[0][t] = acc[1][t] = mfma_f32x4{0, 0, 0, 0};
-  WeightStep v0, v1;
-  stage(0, 0);
-  for (uint32_t turn4 = 0; turn4 < turns; turn4 += 4u) {
-    const uint32_t s = s0 + turn4 / 4u;
-    if (s < whole) {
-      load_weights<kFp4, false>(w0, s, v0);
-      load_weights<kFp4, false>(w1, s, v1);
-    } else if (s < s1) {
-      load_weights<kFp4, true>(w0, s, v0);
-      load_weights<kFp4, true>(w1, s, v1);
-    }
-    quad_transpose(v0.v);
-    quad_transpose(v1.v);
-    each<4>([&](auto j) __attribute__((always_inline)) {
-      wait_vm<0>();
-      __syncthreads();  // block j is in, and the other buffer has been read
-      stage(turn4 + j + 1u, (j + 1u) & 1u);
-      if (s < s1) {
-        const uint8_t* in = mine + (j & 1u) * kBuf + (r & 3u) * kWideLoad + (4u * (r >> 2) + 16u * h) * 16u;
-        each<4>([&](auto k) __attribute__((always_inline)) {
-          const u32x4 o0 = weight_operand<kFp4>(v0, j, k), o1 = weight_operand<kFp4>(v1, j, k);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const u32x4 x = *(const u32x4*)(in + t * 4u * kWideLoad + 16u * k);
-            acc[0][t] = mfma16(o0, x, acc[0][t]);
-            acc[1][t] = mfma16(o1, x, acc[1][t]);
-          }
-        });
-      }
+  WeightStep w[MT];
+  // tiles past the last row repeat the first one and are not stored
+  auto codes = [&](uint32_t s, WeightStep* to) __attribute__((always_inline)) {
+    each<MT>([&](auto m) __attribute__((always_inline)) {
+      const uint64_t at = row0 + 16u * m;
+      const WeightTile<kFp4> t(a.codes, a.scales, at < a.rows ? at : row0, a.rows, a.cols);
+      if (s < whole)
+        load_weights<kFp4, false>(t, s, to[m]);
+      else
+        load_weights<kFp4, true>(t, s, to[m]);
     });
+  };
+  mfma_f32x4 acc[MT][NT];
+  each<MT * NT>([&](auto i) __attribute__((always_inline)) { acc[i / NT][i % NT] = mfma_f32x4{0, 0, 0, 0}; });
+  if (s0 < s1) {
+    codes(s0, w);
+    stage(s0, std::integral_constant<int, 0>{}, 0);
   }
-  // the column parts' sums, in order
+  for (uint32_t s = s0; s < s1; ++s) {
+    each<MT>([&](auto m) __attribute__((always_inline)) { quad_transpose(w[m].v); });
+    WeightStep next[MT];
+    each<4>([&](auto j) __attribute__((always_inline)) {
+      wait_lgkm0();  // the other buffer has been read
+      wait_vm<0>();  // and this one is in
+      wave_lds_sync();
+      if constexpr (j < 3) {
+        stage(s, std::integral_constant<int, j + 1>{}, (j + 1u) & 1u);
+        if constexpr (j == 0) codes(s + 1u < s1 ? s + 1u : s, next);
+      } else if (s + 1u < s1) {
+        stage(s + 1u, std::integral_constant<int, 0>{}, 0);
+      }
+      const uint8_t* in = mine + (j & 1u) * kBuf + (r & 3u) * kWideLoad + (4u * (r >> 2) + 16u * h) * 16u;
+      each<4>([&](auto k) __attribute__((always_inline)) {
+        u32x4 xs[NT];
+        each<NT>([&](auto t) __attribute__((always_inline)) { xs[t] = *(const u32x4*)(in + t * 4u * kWideLoad + 16u * k); });
+        each<MT>([&](auto m) __attribute__((always_inline)) {
+          const u32x4 op = weight_operand<kFp4>(w[m], j, k);
+          each<NT>([&](auto t) __attribute__((always_inline)) { acc[m][t] = mfma16(op, xs[t], acc[m][t]); });
+        });
+      });
+    });
+    each<MT>([&](auto m) __attribute__((always_inline)) { w[m] = next[m]; });
+  }
+  // the waves' sums, in order
   __syncthreads();
-  mfma_f32x4* const part = (mfma_f32x4*)lds;  // [KG][RT][2][NT][kWave]
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) part[((wave * 2u + m) * NT + t) * kWave + lane] = acc[m][t];
+  mfma_f32x4* const part = (mfma_f32x4*)lds;  // [KG][MT][NT][kWave]
+  each<MT * NT>([&](auto i) __attribute__((always_inline)) {
+    part[(kg * MT * NT + i) * kWave + lane] = acc[i / NT][i % NT];
+  });
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < RT * 2u * NT * kWave; i += kWave * RT * KG) {
+  for (uint32_t i = threadIdx.x; i < MT * NT * kWave; i += kWave * KG) {
     mfma_f32x4 s = part[i];
 #pragma unroll
-    for (uint32_t v = 1; v < KG; ++v) s += part[v * (RT * 2u * NT * kWave) + i];
-    // kg 0's waves are 0 .. RT - 1, so i is (rt, m, t, lane)
-    const uint32_t l = i % kWave, t = i / kWave % NT, m = i / (kWave * NT) % 2u, q = i / (kWave * NT * 2u);
+    for (uint32_t v = 1; v < KG; ++v) s += part[v * (MT * NT * kWave) + i];
+    const uint32_t l = i % kWave, t = i / kWave % NT, m = i / (kWave * NT);
     const uint32_t b = b0 + 16u * t + (l & 15u);
-    const uint64_t y0 = ((uint64_t)blockIdx.x * RT + q) * 32u + 16u * m + 4u * (l >> 4);
+    const uint64_t y0 = row0 + 16u * m + 4u * (l >> 4);
     if (b < a.batch) {
 #pragma unroll
       for (uint32_t k = 0; k < 4; ++k)
@@ -290,12 +294,34 @@ void launch_rows(const Fp4Args& a, uint32_t row_blocks, uint32_t batch_blocks, h
     k_fp4_gemv<QUAD, true, 1><<<grid, kWave * waves, lds, s>>>(a);
 }
 
-template <int NT, int RT, int KG>
+template <int MT, int NT, int KG>
 void launch_wide(const Fp4Args& a, hipStream_t s) {
-  const uint32_t row_blocks = (uint32_t)((a.rows + RT * 32u - 1u) / (RT * 32u));
-  const size_t in = (size_t)KG * 2u * NT * 4u * kWideLoad, sums = (size_t)KG * RT * 2u * NT * 1024u;
-  k_fp4_wide<NT, RT, KG><<<dim3(row_blocks, (a.batch + 16u * NT - 1u) / (16u * NT)), kWave * RT * KG,
+  const uint32_t row_blocks = (uint32_t)((a.rows + MT * 16u - 1u) / (MT * 16u));
+  const size_t in = (size_t)KG * 2u * NT * 4u * kWideLoad, sums = (size_t)KG * MT * NT * 1024u;
+  k_fp4_wide<MT, NT, KG><<<dim3(row_blocks, (a.batch + 16u * NT - 1u) / (16u * NT)), kWave * KG,
                            in > sums ? in : sums, s>>>(a);
+}
+
+// Every block reads the inputs of its batch tiles whole, so the tallest tile whose
+// blocks still fill the compute units is the fastest (6144 x 24576, batch 64: 64
+// rows 73.7 us, 32 rows 58.6; 14336 x 4096: 22.3, 28.4; 4096 x 4096 at two
+// tiles of inputs, 32 rows: 10.2 against 12.3 with four).  Blocks of four waves
+// where two or more of them go on a compute unit.
+void launch_wide_for(const Fp4Args& a, hipStream_t s) {
+  auto blocks = [&](uint32_t mt, uint32_t nt) {
+    return (a.rows + 16u * mt - 1u) / (16u * mt) * ((a.batch + 16u * nt - 1u) / (16u * nt));
+  };
+  const uint64_t enough = cu_count() * 5u / 8u;
+  if (a.batch > 32 && blocks(4, 4) >= enough)
+    launch_wide<4, 4, 4>(a, s);
+  else if (a.batch > 32 && blocks(2, 4) >= enough)
+    launch_wide<2, 4, 4>(a, s);
+  else if (blocks(2, 2) >= 2u * enough)
+    launch_wide<2, 2, 4>(a, s);
+  else if (blocks(2, 2) >= enough)
+    launch_wide<2, 2, 8>(a, s);
+  else
+    launch_wide<1, 2, 8>(a, s);
 }
 
 uint32_t piece_blocks(uint64_t pieces) {
@@ -348,9 +374,7 @@ extern "C" int wc_fp4_gemv(const uint8_t* d_codes, const uint8_t* d_scales, uint
     wc::launch_rows<true>(a, rb, 1, s);
   else if (batch <= 16 || cols % 8u)
     wc::launch_rows<false>(a, rb, (batch + 15u) / 16u, s);
-  else if (batch <= 32)
-    wc::launch_wide<2, 1, 8>(a, s);
   else
-    wc::launch_wide<4, 2, 4>(a, s);
+    wc::launch_wide_for(a, s);
   return wc::launched();
 }

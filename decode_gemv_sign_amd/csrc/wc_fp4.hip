@@ -112,7 +112,8 @@ __global__ __launch_bounds__(kWave * 16) void k_fp4_gemv(Fp4Args a) {
   const uint64_t row0 = (uint64_t)blockIdx.x * kRowTile;
   const uint32_t b0 = blockIdx.y * kRowTile;
   const uint32_t nb = a.batch - b0 < kRowTile ? a.batch - b0 : kRowTile;
-  const WeightTile<kFp4> w(a.codes, a.scales, row0, a.rows, a.cols);
+  const WeightLane<kFp4> lw(a.cols);
+  const WeightTile<kFp4> w(a.codes, a.scales, row0, a.rows, lw);
   const InputTile<QUAD, ANY> x(a.x + (uint64_t)b0 * a.cols, nb, a.cols,
                                [&](uint32_t i) { return i < nb ? i : nb - 1u; });
   Sums<QUAD> acc;
@@ -136,7 +137,7 @@ __global__ __launch_bounds__(kWave * 16) void k_fp4_gemv(Fp4Args a) {
   step_batches<U, Slot>(
       (s1 < whole ? s1 : whole) - s0,
       [&](uint32_t q, Slot& s) __attribute__((always_inline)) {
-        load_weights<kFp4, false>(w, s0 + q, s.w);
+        load_weights<kFp4, false>(lw, w, s0 + q, s.w);
         each<4>([&](auto j) __attribute__((always_inline)) {
           load_inputs<kFp4, false>(x, s0 + q, j, s.x[j]);
         });
@@ -144,7 +145,7 @@ __global__ __launch_bounds__(kWave * 16) void k_fp4_gemv(Fp4Args a) {
       use);
   if (s1 > whole && s1 > s0) {  // the short last step
     Slot s;
-    load_weights<kFp4, true>(w, whole, s.w);
+    load_weights<kFp4, true>(lw, w, whole, s.w);
     each<4>([&](auto j) __attribute__((always_inline)) { load_inputs<kFp4, true>(x, whole, j, s.x[j]); });
     use(s);
   }
@@ -203,16 +204,17 @@ __global__ __launch_bounds__(kWave * KG) void k_fp4_wide(Fp4Args a) {
       });
     }
   };
+  const WeightLane<kFp4> lw(a.cols);
   WeightStep w[MT];
   // tiles past the last row repeat the first one and are not stored
   auto codes = [&](uint32_t s, WeightStep* to) __attribute__((always_inline)) {
     each<MT>([&](auto m) __attribute__((always_inline)) {
       const uint64_t at = row0 + 16u * m;
-      const WeightTile<kFp4> t(a.codes, a.scales, at < a.rows ? at : row0, a.rows, a.cols);
+      const WeightTile<kFp4> t(a.codes, a.scales, at < a.rows ? at : row0, a.rows, lw);
       if (s < whole)
-        load_weights<kFp4, false>(t, s, to[m]);
+        load_weights<kFp4, false>(lw, t, s, to[m]);
       else
-        load_weights<kFp4, true>(t, s, to[m]);
+        load_weights<kFp4, true>(lw, t, s, to[m]);
     });
   };
   mfma_f32x4 acc[MT][NT];

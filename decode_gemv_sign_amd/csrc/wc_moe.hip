@@ -2,32 +2,38 @@
 // launches (include/wc_moe.h defines the operator):
 //   k_moe_router   logits of every token and expert (matrix cores)
 //   k_moe_gate_up  every block chooses the experts again from the logits
-//                  (a few waves' work, cheaper than a launch), then walks
-//                  (expert, 16 intermediate rows) items: gate and up products,
-//                  silu(gate) * up * weight into the workspace
+//                  (a few waves' work, cheaper than a launch), then works on its
+//                  share of the (expert, 16 intermediate rows) tiles: gate and up
+//                  products, silu(gate) * up * weight into the workspace
 //   k_moe_down     16 output rows per block: the sum over all chosen experts,
-//                  kept in the block, so that nothing is added through memory
-//                  and the result does not depend on which block ends first
+//                  kept in the block (or in two or four that split the experts
+//                  where the rows are too few for the card), so that nothing is
+//                  added through memory in an order that could change
 // Each expert's set of tokens is one 64-bit mask, which is what bounds the
 // number of tokens of a call.
 #include "wc_launch.h"
 #include "wc_moe.h"
 #include "wc_skinny.h"
 
+#ifndef WC_DU
+#define WC_DU 1
+#define WC_DUB 2
+#endif
+
 namespace wc {
 
 constexpr uint32_t kMoeExperts = WC_MOE_MAX_EXPERTS;
 constexpr uint32_t kMoePlaces = WC_MOE_MAX_TOKENS * WC_MOE_MAX_TOP_K;  // (token, choice) pairs
 constexpr uint32_t kRouterWaves = 16;
-constexpr uint32_t kUpWaves = 4;     // waves per block of k_moe_gate_up
+constexpr uint32_t kUpWaves = 16;    // waves per block of k_moe_gate_up, one block per compute unit
 constexpr uint32_t kDownWaves = 16;  // and of k_moe_down
+constexpr uint32_t kMaxParts = 4;    // blocks of k_moe_down on the same rows
 
-// The products take an expert's tokens in units: of up to 32 in k_moe_gate_up,
-// of up to 8 in k_moe_down.
-constexpr uint32_t kUpTokens = 32;
+// The products take an expert's tokens in units: in k_moe_gate_up of up to 16,
+// and of no more than its LDS holds inputs for; in k_moe_down of up to 8, each as
+// a high and a low part.
+constexpr uint32_t kUpInputs = 128u * 1024u;  // bytes of LDS
 constexpr uint32_t kDownTokens = 8;
-constexpr uint32_t kUpUnits = kMoeExperts + kMoePlaces / kUpTokens;
-constexpr uint32_t kDownUnits = kMoeExperts + kMoePlaces / kDownTokens;
 
 struct MoeUnit {
   uint16_t expert;
@@ -38,7 +44,7 @@ struct MoeUnit {
 // The choice, as k_moe_down needs it.
 struct MoeRoute {
   uint32_t units;
-  MoeUnit unit[kDownUnits];
+  MoeUnit unit[kMoePlaces];
   uint8_t token[kMoePlaces];  // by place
 };
 
@@ -53,48 +59,68 @@ struct MoeArgs {
   uint16_t* y;
   int32_t* ids;
   float* weights;
-  float* logits;  // [tokens][experts]
+  float* logits;      // [tokens][experts]
   MoeRoute* route;
-  uint16_t* act;  // operands of k_moe_down: by unit, block, k, lane (act_at below)
+  uint16_t* act;      // operands of k_moe_down (act_at below)
+  uint32_t* arrived;  // blocks of k_moe_down that are done, by row tile
+  float* partial;     // their sums, [row tile][part][tokens][16]
   uint32_t tokens, hidden, inter, experts, top_k, scoring, renorm;
+  uint32_t up_tokens;   // most tokens of a unit of k_moe_gate_up
   uint32_t act_blocks;  // of 128 columns per unit: inter rounded up to whole steps, the rest 0
   uint32_t down_fp4;    // the order of the columns in a step
-  uint32_t most_units;  // bound of MoeRoute::units
+  uint32_t parts;       // blocks of k_moe_down on the same rows
   float scale;
 };
 
 // Byte offsets in the caller's workspace.
 struct MoeWork {
-  size_t logits, route, act, total;
+  size_t logits, route, act, arrived, partial, total;
 };
 
-// Units of k_moe_down at most: every chosen expert's first, and one more for
-// every kDownTokens further pairs.
-inline uint32_t moe_units(const wc_moe_shape& s, uint32_t size) {
-  const uint32_t pairs = s.tokens * s.top_k;
-  return (pairs < s.experts ? pairs : s.experts) + (s.tokens > size ? pairs / size : 0u);
+inline uint32_t moe_blocks(uint32_t cols, uint32_t step_cols) {  // of 128 columns, in whole steps
+  return (cols + step_cols - 1u) / step_cols * (step_cols / 128u);
 }
 
-inline uint32_t moe_act_blocks(uint32_t inter, uint32_t step_cols) {
-  return (inter + step_cols - 1u) / step_cols * (step_cols / 128u);
+// Most tokens of a unit of k_moe_gate_up: what its LDS holds in whole 4-bit steps.
+inline uint32_t moe_up_tokens(uint32_t hidden) {
+  const uint32_t n = kUpInputs / (moe_blocks(hidden, kStepCols<kFp4>) * 256u);
+  return n > 16u ? 16u : n;
 }
 
 inline MoeWork moe_work(const wc_moe_shape& s) {
   MoeWork m;
+  const uint64_t tiles = (s.hidden + 15u) / 16u;
   m.logits = 0;
   m.route = pad16(m.logits + 4ull * s.tokens * s.experts);
   m.act = pad16(m.route + sizeof(MoeRoute));
-  // 4 KB a block; whole 4-bit steps, so that the size does not go by the kind
-  m.total = m.act + 4096ull * moe_units(s, kDownTokens) * moe_act_blocks(s.inter, kStepCols<kFp4>);
+  // 512 bytes a pair and block; whole 4-bit steps, so that the size does not go by the kind
+  m.arrived = m.act + 512ull * s.tokens * s.top_k * moe_blocks(s.inter, kStepCols<kFp4>);
+  m.partial = pad16(m.arrived + 4u * tiles);
+  m.total = m.partial + 64ull * kMaxParts * s.tokens * tiles;
   return m;
 }
 
-// Where column c of a unit's input row n stands in `act`: as the lanes of
-// k_moe_down hold it (wc_skinny.h), so that its loads are contiguous.
-__device__ __forceinline__ uint64_t act_at(const MoeArgs& a, uint32_t unit, uint32_t n, uint32_t c) {
-  const uint32_t block = a.down_fp4 ? (c >> 9) * 4u + (c >> 5 & 3u) : c >> 7;
-  const uint32_t h = a.down_fp4 ? c >> 7 & 3u : c >> 5 & 3u;
-  return (((uint64_t)unit * a.act_blocks + block) * 4u + (c >> 3 & 3u)) * 512u + (n + 16u * h) * 8u + (c & 7u);
+// Columns of a row go to the lanes of the matrix operands in pieces of 8
+// (wc_skinny.h): piece q of a row is piece k of lanes h in a block.
+struct Piece {
+  uint32_t block, k, h;
+};
+template <bool FP4>
+__device__ __forceinline__ Piece piece_of(uint32_t q) {
+  return FP4 ? Piece{(q >> 6) * 4u + (q >> 2 & 3u), q & 3u, q >> 4 & 3u} : Piece{q >> 4, q & 3u, q >> 2 & 3u};
+}
+
+// Where pieces of the operands of `count` rows stand, in pieces: [block][k][h][row],
+// so that what 64 lanes ask for at a time is contiguous and no larger than the
+// rows there are.
+__device__ __forceinline__ uint32_t operand_at(uint32_t block, uint32_t k, uint32_t h, uint32_t count, uint32_t row) {
+  return ((block * 4u + k) * 4u + h) * count + row;
+}
+
+// `act` of a unit of k_moe_down: 2 * count rows, of token i the high part at 2 i
+// and the low part at 2 i + 1.
+__device__ __forceinline__ u32x4* act_of(const MoeArgs& a, const MoeUnit& u) {
+  return (u32x4*)a.act + (uint64_t)u.place * (32u * a.act_blocks);
 }
 
 // ---- router ------------------------------------------------------------------
@@ -106,8 +132,14 @@ __global__ __launch_bounds__(kWave * kRouterWaves) void k_moe_router(MoeArgs a) 
   const uint32_t lane = (uint32_t)lane_id(), wave = (uint32_t)wave_in_block();
   const uint32_t r = lane & 15u;
   const uint32_t e0 = blockIdx.x * kRowTile, t0 = blockIdx.y * kRowTile;
+  // the counters that k_moe_down's blocks count in
+  const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x;
+  for (uint32_t i = block * (kWave * kRouterWaves) + threadIdx.x; i < (a.hidden + 15u) / 16u;
+       i += gridDim.x * gridDim.y * (kWave * kRouterWaves))
+    a.arrived[i] = 0;
   constexpr int kKind = ANY ? kBf16Any : kBf16;
-  const WeightTile<kKind> w(a.router, nullptr, e0, a.experts, a.hidden);
+  const WeightLane<kKind> lw(a.hidden);
+  const WeightTile<kKind> w(a.router, nullptr, e0, a.experts, lw);
   const InputTile<false, ANY> x(a.x, a.tokens, a.hidden,
                                 [&](uint32_t i) { return t0 + i < a.tokens ? t0 + i : a.tokens - 1u; });
   mfma_f32x4 acc = {0, 0, 0, 0};
@@ -126,13 +158,13 @@ __global__ __launch_bounds__(kWave * kRouterWaves) void k_moe_router(MoeArgs a) 
   step_batches<2, Slot>(
       s1 - s0,
       [&](uint32_t q, Slot& s) __attribute__((always_inline)) {
-        load_weights<kKind, false>(w, s0 + q, s.w);
+        load_weights<kKind, false>(lw, w, s0 + q, s.w);
         load_inputs<kKind, false>(x, s0 + q, 0, s.x);
       },
       use);
   if (wave == kRouterWaves - 1u && whole * kStepCols<kKind> < a.hidden) {
     Slot s;
-    load_weights<kKind, true>(w, whole, s.w);
+    load_weights<kKind, true>(lw, w, whole, s.w);
     load_inputs<kKind, true>(x, whole, 0, s.x);
     use(s);
   }
@@ -200,14 +232,13 @@ __device__ inline float key_value(uint32_t k) {
 }
 
 struct MoeChoice {
-  uint64_t mask[kMoeExperts];     // tokens of each expert
-  uint16_t first[kMoeExperts];    // its first place among the chosen pairs
-  uint16_t down_first[kMoeExperts];  // and its first unit of k_moe_down
-  MoeUnit unit[kUpUnits];         // units of k_moe_gate_up
-  uint32_t units, down_units;
-  float weight[kMoePlaces];       // by [token][choice]
-  int16_t id[kMoePlaces];
-  float place_weight[kMoePlaces]; // by place
+  uint64_t mask[kMoeExperts];        // tokens of each expert
+  uint16_t first[kMoeExperts];       // its first place among the chosen pairs
+  MoeUnit unit[kMoePlaces];          // units of k_moe_gate_up
+  uint32_t units;
+  int16_t id[kMoePlaces];            // by [token][choice]
+  float weight[kMoePlaces];
+  float place_weight[kMoePlaces];    // by place
   uint8_t place_token[kMoePlaces];
 };
 
@@ -319,20 +350,16 @@ __device__ inline void choose_all(const MoeArgs& a, MoeChoice& c, MoeRoute* rout
     for (uint32_t e0 = 0; e0 < a.experts; e0 += kWave) {
       const uint32_t e = e0 + lane;
       const uint32_t n = e < a.experts ? (uint32_t)__popcll(c.mask[e]) : 0u;
-      // three sums of at most 1024 in one scan: places, and units of both kinds
-      const uint32_t nu = (n + kUpTokens - 1u) / kUpTokens, nd = (n + kDownTokens - 1u) / kDownTokens;
-      const uint32_t before = wave_excl_scan_u32(n | nd << 12 | nu << 24);
-      const uint32_t first = places + (before & 0xFFFu);
-      if (e < a.experts) {
-        c.first[e] = (uint16_t)first;
-        c.down_first[e] = (uint16_t)(down + (before >> 12 & 0xFFFu));
-      }
-      fill_units(c.unit, units + (before >> 24), e, first, n, kUpTokens);
-      if (route) fill_units(route->unit, down + (before >> 12 & 0xFFFu), e, first, n, kDownTokens);
-      const uint32_t all = wave_total(n | nd << 12 | nu << 24);
-      places += all & 0xFFFu;
-      down += all >> 12 & 0xFFFu;
-      units += all >> 24;
+      const uint32_t nu = (n + a.up_tokens - 1u) / a.up_tokens, nd = (n + kDownTokens - 1u) / kDownTokens;
+      const uint32_t pb = wave_excl_scan_u32(n), ub = wave_excl_scan_u32(nu | nd << 16);
+      const uint32_t first = places + pb;
+      if (e < a.experts) c.first[e] = (uint16_t)first;
+      fill_units(c.unit, units + (ub & 0xFFFFu), e, first, n, a.up_tokens);
+      if (route) fill_units(route->unit, down + (ub >> 16), e, first, n, kDownTokens);
+      const uint32_t all = wave_total(nu | nd << 16);
+      places += wave_total(n);
+      units += all & 0xFFFFu;
+      down += all >> 16;
     }
     if (lane == 0) {
       c.units = units;
@@ -359,131 +386,157 @@ __device__ inline void choose_all(const MoeArgs& a, MoeChoice& c, MoeRoute* rout
 
 // ---- gate and up ---------------------------------------------------------------
 
-// One item: 16 rows of gate and the same 16 of up of one expert, with NT tiles
-// of 16 of a unit's tokens; wave `part` of SPLIT takes its run of steps.
-template <int KIND, bool ANY, int NT, int U>
-__device__ __forceinline__ void gate_up_item(const MoeArgs& a, const MoeChoice& c, const MoeUnit& unit,
-                                             uint32_t row0, uint32_t part, uint32_t split,
-                                             mfma_f32x4 g[NT], mfma_f32x4 u[NT]) {
-  const uint64_t base = (uint64_t)unit.expert * 2u * a.inter;
-  // rows past `inter` repeat the last one: sums that are not used
-  const WeightTile<KIND> wg(a.gu, a.gu_scales, base + row0, base + a.inter, a.hidden);
-  const WeightTile<KIND> wu(a.gu, a.gu_scales, base + a.inter + row0, base + 2u * a.inter, a.hidden);
-  auto input = [&](int t) __attribute__((always_inline)) {
-    return InputTile<false, ANY>(a.x, a.tokens, a.hidden, [&](uint32_t i) {
-      const uint32_t m = 16u * (uint32_t)t + i;  // columns past the unit's tokens repeat its last one
-      return (uint32_t)c.place_token[unit.place + (m < unit.count ? m : unit.count - 1u)];
-    });
-  };
-  const InputTile<false, ANY> x0 = input(0), x1 = input(NT - 1);
-#pragma unroll
-  for (int t = 0; t < NT; ++t) g[t] = u[t] = mfma_f32x4{0, 0, 0, 0};
-  constexpr int kB = kBlocks<KIND>;
-  struct Slot {
-    WeightStep g, u;
-    InputBlock<false> x[NT][kB];
-  };
-  auto use = [&](Slot& s) __attribute__((always_inline)) {
-    quad_transpose(s.g.v);
-    quad_transpose(s.u.v);
-    each<kB>([&](auto j) __attribute__((always_inline)) {
-      each<NT>([&](auto t) __attribute__((always_inline)) { quad_transpose(s.x[t][j].v); });
-      each<4>([&](auto k) __attribute__((always_inline)) {
-        const u32x4 og = weight_operand<KIND>(s.g, j, k), ou = weight_operand<KIND>(s.u, j, k);
-        each<NT>([&](auto t) __attribute__((always_inline)) {
-          g[t] = mfma16(og, s.x[t][j].v[k], g[t]);
-          u[t] = mfma16(ou, s.x[t][j].v[k], u[t]);
-        });
-      });
-    });
-  };
-  auto load = [&](auto tail, uint32_t step, Slot& s) __attribute__((always_inline)) {
-    load_weights<KIND, tail>(wg, step, s.g);
-    load_weights<KIND, tail>(wu, step, s.u);
-    each<kB>([&](auto j) __attribute__((always_inline)) {
-      load_inputs<KIND, tail>(x0, step, j, s.x[0][j]);
-      if constexpr (NT == 2) load_inputs<KIND, tail>(x1, step, j, s.x[1][j]);
-    });
-  };
-  const uint32_t whole = a.hidden / kStepCols<KIND>;
-  const uint32_t steps = (a.hidden + kStepCols<KIND> - 1u) / kStepCols<KIND>;
-  const uint32_t s0 = part * steps / split, s1 = (part + 1u) * steps / split;
-  step_batches<U, Slot>(
-      (s1 < whole ? s1 : whole) - s0,
-      [&](uint32_t q, Slot& s) __attribute__((always_inline)) { load(std::false_type{}, s0 + q, s); }, use);
-  if (s1 > whole && s1 > s0) {  // the short last step
-    Slot s;
-    load(std::true_type{}, whole, s);
-    use(s);
-  }
-}
-
-// MANY: more than 16 tokens in the call, so units may fill two tiles.
-// SPLIT waves share an item; the block works on kUpWaves / SPLIT of them.
-template <int KIND, bool ANY, bool MANY, uint32_t SPLIT>
-__global__ __launch_bounds__(kWave * kUpWaves, MANY ? 2 : 3) void k_moe_gate_up(MoeArgs a) {
-  constexpr int NT = MANY ? 2 : 1;
-  constexpr uint32_t kItems = kUpWaves / SPLIT;
+// A block's share of the tiles (unit, 16 rows of gate and the same 16 of up) is
+// one run of them, unit by unit.  The inputs of a unit's tokens come to LDS in
+// operand order; then the steps of all the block's tiles of that unit, tile by
+// tile, are shared out evenly: each wave takes one run of steps, and a tile that
+// several waves worked on is joined in LDS, in wave order.
+template <int KIND, int U>
+__global__ __launch_bounds__(kWave * kUpWaves) void k_moe_gate_up(MoeArgs a) {
   __shared__ MoeChoice c;
-  __shared__ mfma_f32x4 sums[kUpWaves][2 * NT][kWave];
+  extern __shared__ __attribute__((aligned(16))) u32x4 inputs[];  // then sums[kUpWaves][2][2][kWave]
+  mfma_f32x4* const sums = (mfma_f32x4*)inputs;
   choose_all(a, c, blockIdx.x == 0 ? a.route : nullptr);
   const uint32_t lane = (uint32_t)lane_id(), wave = (uint32_t)wave_in_block();
-  const uint32_t slot = wave / SPLIT, part = wave % SPLIT;
-  const uint32_t tiles = (a.inter + kRowTile - 1) / kRowTile, items = c.units * tiles;
-  for (uint32_t base = blockIdx.x * kItems; base < items; base += gridDim.x * kItems) {
-    const uint32_t item = base + slot;
-    const bool on = item < items;
-    const MoeUnit unit = c.unit[on ? item / tiles : 0u];
-    const uint32_t row0 = item % tiles * kRowTile;
-    if (on) {
-      if (NT == 1 || unit.count <= 16u) {
-        mfma_f32x4 g[1], u[1];
-        gate_up_item<KIND, ANY, 1, KIND == kFp4 ? 1 : 2>(a, c, unit, row0, part, SPLIT, g, u);
-        sums[wave][0][lane] = g[0];
-        sums[wave][1][lane] = u[0];
-      } else {
-        mfma_f32x4 g[NT], u[NT];
-        gate_up_item<KIND, ANY, NT, 1>(a, c, unit, row0, part, SPLIT, g, u);
+  const uint32_t r = lane & 15u, h = lane >> 4;
+  constexpr bool kIsFp4 = KIND == kFp4;
+  constexpr int kB = kBlocks<KIND>;
+  const uint32_t tiles = (a.inter + kRowTile - 1u) / kRowTile, items = c.units * tiles;
+  const uint32_t whole = a.hidden / kStepCols<KIND>;
+  const uint32_t steps = (a.hidden + kStepCols<KIND> - 1u) / kStepCols<KIND>;
+  const WeightLane<KIND> lw(a.hidden);
+  const uint32_t end = (uint32_t)((uint64_t)(blockIdx.x + 1u) * items / gridDim.x);
+
+  // The tile's sums g and u, for the unit's tokens: into act.
+  auto finish = [&](const MoeUnit& unit, uint32_t tile, mfma_f32x4 g, mfma_f32x4 u) __attribute__((always_inline)) {
+    if (r >= unit.count) return;
+    const uint32_t place = unit.place + r, rank = place - c.first[unit.expert];
+    const uint32_t n = (uint32_t)__popcll(c.mask[unit.expert]);
+    const uint32_t m0 = rank / kDownTokens * kDownTokens;  // its unit of k_moe_down
+    const uint32_t rows = 2u * (n - m0 < kDownTokens ? n - m0 : kDownTokens);
+    uint2* const act = (uint2*)act_of(a, MoeUnit{0, (uint16_t)(c.first[unit.expert] + m0), 0});
+    auto put = [&](uint32_t col, uint2 hi, uint2 lo) __attribute__((always_inline)) {
+      const Piece p = a.down_fp4 ? piece_of<true>(col >> 3) : piece_of<false>(col >> 3);
+      const uint32_t at = 2u * operand_at(p.block, p.k, p.h, rows, 2u * (rank - m0)) + (col >> 2 & 1u);
+      act[at] = hi;
+      act[at + 2u] = lo;
+    };
+    const float weight = c.place_weight[place];
+    const uint32_t i0 = tile * kRowTile + 4u * h;
+    uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          sums[wave][2 * t][lane] = g[t];
-          sums[wave][2 * t + 1][lane] = u[t];
-        }
+    for (int k = 0; k < 4; ++k) {
+      // weight * silu(gate) * up, as the sum of two BF16 (16 bits of it)
+      const float v = i0 + k < a.inter ? g[k] / (1.0f + expf(-g[k])) * u[k] * weight : 0.0f;
+      hi[k] = bf16_of(v);
+      const float rest = v - __uint_as_float(hi[k] << 16);
+      lo[k] = rest == rest ? bf16_of(rest) : 0u;  // v infinite or NaN: the high part says so
+    }
+    put(i0, uint2{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16}, uint2{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16});
+    if (tile + 1u == tiles)
+      for (uint32_t i = i0 + kRowTile; i < a.act_blocks * 128u; i += kRowTile) put(i, uint2{0, 0}, uint2{0, 0});
+  };
+
+  for (uint32_t item = (uint32_t)((uint64_t)blockIdx.x * items / gridDim.x); item < end;) {
+    const uint32_t un = item / tiles, tile0 = item - un * tiles;
+    const uint32_t count = end - item < tiles - tile0 ? end - item : tiles - tile0;  // tiles of the run
+    item += count;
+    const MoeUnit unit = c.unit[un];
+    // inputs, as [block][k][h][token]
+    const uint32_t pieces = steps * kB * 16u;
+    for (uint32_t i = threadIdx.x; i < pieces * unit.count; i += kWave * kUpWaves) {
+      const uint32_t t = i / pieces, q = i - t * pieces;
+      const uint16_t* row = a.x + (uint64_t)c.place_token[unit.place + t] * a.hidden;
+      const Piece p = piece_of<kIsFp4>(q);
+      inputs[operand_at(p.block, p.k, p.h, unit.count, t)] =
+          8u * q + 8u <= a.hidden ? *(const u32x4_any*)(row + 8u * q) : load8(row, 8u * q, a.hidden);
+    }
+    __syncthreads();
+    const uint32_t total = count * steps;
+    const uint32_t f0 = wave * total / kUpWaves, f1 = (wave + 1u) * total / kUpWaves;
+    const uint64_t gate = (uint64_t)unit.expert * 2u * a.inter, rows = (uint64_t)a.experts * 2u * a.inter;
+    const uint32_t mine = r < unit.count ? r : unit.count - 1u;  // columns past the tokens repeat the last one
+    mfma_f32x4 g = {0, 0, 0, 0}, u = {0, 0, 0, 0};
+    mfma_f32x4 g0 = g, u0 = u;  // of the wave's first tile, when it is not the last
+    uint32_t done = 0;          // whether that is so
+    uint32_t lt = f0 / steps, ls = f0 - lt * steps;  // the next step to load: tile, step
+    uint32_t ut = lt, us = ls;                       // and to use
+    const bool starts = ls == 0;  // the first tile has no steps before this wave
+    struct Slot {
+      WeightStep g, u;
+    };
+    step_batches<U, Slot>(
+        f1 - f0,
+        [&](uint32_t, Slot& s) __attribute__((always_inline)) {
+          const uint64_t row = (uint64_t)(tile0 + lt) * kRowTile;
+          const WeightTile<KIND> wg(a.gu, a.gu_scales, gate + row, rows, lw);
+          const WeightTile<KIND> wu(a.gu, a.gu_scales, gate + a.inter + row, rows, lw);
+          if (ls < whole) {
+            load_weights<KIND, false>(lw, wg, ls, s.g);
+            load_weights<KIND, false>(lw, wu, ls, s.u);
+          } else {
+            load_weights<KIND, true>(lw, wg, ls, s.g);
+            load_weights<KIND, true>(lw, wu, ls, s.u);
+          }
+          if (++ls == steps) {
+            ls = 0;
+            ++lt;
+          }
+        },
+        [&](Slot& s) __attribute__((always_inline)) {
+          quad_transpose(s.g.v);
+          quad_transpose(s.u.v);
+          each<kB>([&](auto j) __attribute__((always_inline)) {
+            each<4>([&](auto k) __attribute__((always_inline)) {
+              const u32x4 x = inputs[operand_at(us * kB + j, k, h, unit.count, mine)];
+              g = mfma16(weight_operand<KIND>(s.g, j, k), x, g);
+              u = mfma16(weight_operand<KIND>(s.u, j, k), x, u);
+            });
+          });
+          if (++us == steps) {  // the tile's last step
+            if (starts || done) {
+              finish(unit, tile0 + ut, g, u);
+            } else {
+              g0 = g;
+              u0 = u;
+            }
+            done = 1;
+            us = 0;
+            ++ut;
+            g = u = mfma_f32x4{0, 0, 0, 0};
+          }
+        });
+    // Tiles shared with other waves: sums[wave][0] is the wave's part of its first
+    // tile, [1] of its last one.  Tile t's steps t * steps .. are those of waves
+    // w0 .. w1, and w1 joins them.
+    __syncthreads();
+    if (f1 > f0) {
+      const bool ended = us == 0;  // its last tile is whole, or ends here
+      if (!starts && done) {
+        sums[(wave * 4u + 0u) * kWave + lane] = g0;
+        sums[(wave * 4u + 1u) * kWave + lane] = u0;
+      }
+      if (!ended) {
+        const uint32_t slot = !starts && !done ? 0u : 2u;  // the first tile itself, or a later one
+        sums[(wave * 4u + slot) * kWave + lane] = g;
+        sums[(wave * 4u + slot + 1u) * kWave + lane] = u;
       }
     }
     __syncthreads();
-    // wave `part` of an item finishes its tiles part, part + SPLIT, ..
-    for (uint32_t t = part; on && 16u * t < unit.count; t += SPLIT) {
-      mfma_f32x4 sg = sums[slot * SPLIT][2 * t][lane], su = sums[slot * SPLIT][2 * t + 1][lane];
-#pragma unroll
-      for (uint32_t v = 1; v < SPLIT; ++v) {
-        sg += sums[slot * SPLIT + v][2 * t][lane];
-        su += sums[slot * SPLIT + v][2 * t + 1][lane];
+    if (f1 > f0 && !starts && done) {
+      const uint32_t t = f0 / steps;
+      // the first wave with a step of tile t: the last w with w * total / kUpWaves <= t * steps
+      uint32_t w0 = wave;
+      while (w0 > 0 && w0 * total / kUpWaves > t * steps) --w0;
+      mfma_f32x4 sg = {0, 0, 0, 0}, su = {0, 0, 0, 0};
+      for (uint32_t v = w0; v <= wave; ++v) {
+        const uint32_t v0 = v * total / kUpWaves;
+        if (v0 == (v + 1u) * total / kUpWaves) continue;  // no steps
+        const uint32_t slot = v0 > t * steps ? 0u : 2u;  // inside its first tile, or at the tile's start or before
+        sg += sums[(v * 4u + slot) * kWave + lane];
+        su += sums[(v * 4u + slot + 1u) * kWave + lane];
       }
-      const uint32_t m = 16u * t + (lane & 15u);
-      if (m < unit.count) {
-        const uint32_t place = unit.place + m, rank = place - c.first[unit.expert];
-        const uint32_t to = c.down_first[unit.expert] + rank / kDownTokens, n = rank % kDownTokens;
-        const float p = c.place_weight[place];
-        const uint32_t i0 = row0 + 4u * (lane >> 4);
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          // weight * silu(gate) * up, as the sum of two BF16 (16 bits of it)
-          const float h = i0 + k < a.inter ? sg[k] / (1.0f + expf(-sg[k])) * su[k] * p : 0.0f;
-          hi[k] = bf16_of(h);
-          const float rest = h - __uint_as_float(hi[k] << 16);
-          lo[k] = rest == rest ? bf16_of(rest) : 0u;  // h infinite or NaN: the high part says so
-        }
-        *(uint2*)(a.act + act_at(a, to, n, i0)) = uint2{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16};
-        *(uint2*)(a.act + act_at(a, to, n + 8u, i0)) = uint2{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16};
-        if (row0 + kRowTile >= a.inter) {
-          for (uint32_t i = i0 + kRowTile; i < a.act_blocks * 128u; i += kRowTile) {
-            *(uint2*)(a.act + act_at(a, to, n, i)) = uint2{0, 0};
-            *(uint2*)(a.act + act_at(a, to, n + 8u, i)) = uint2{0, 0};
-          }
-        }
-      }
+      finish(unit, tile0 + t, sg, su);
     }
     __syncthreads();
   }
@@ -491,20 +544,25 @@ __global__ __launch_bounds__(kWave * kUpWaves, MANY ? 2 : 3) void k_moe_gate_up(
 
 // ---- down ----------------------------------------------------------------------
 
-// 16 rows of y per block.  Steps are (unit, 128 columns) in unit order, a run of
-// them per wave.  A unit's high parts are columns 0..7 of the products, its low
-// parts columns 8..15.  When the unit changes, the sums go to the wave's own
-// [token][16] array in LDS; at the end these are added over the waves.
+// 16 rows of y per block, or per a.parts blocks.  Steps are (unit, columns) in unit
+// order, a run of them per part, and of that per wave.  Lane column n takes the
+// high part of token n & 7 of the unit, or (n >= 8) the low part.  When the unit
+// changes, the sums go to the wave's own [token][16] array in LDS; at the end these
+// are added over the waves, and over the parts by the last block to arrive, in
+// order both.
 template <int KIND, int U>
 __global__ __launch_bounds__(kWave * kDownWaves) void k_moe_down(MoeArgs a) {
   extern __shared__ __attribute__((aligned(16))) float ysum[];  // [kDownWaves][tokens][16]
-  __shared__ MoeUnit unit[kDownUnits];
+  __shared__ MoeUnit unit[kMoePlaces];
   __shared__ uint8_t token[kMoePlaces];
+  __shared__ uint32_t before;
   const uint32_t lane = (uint32_t)lane_id(), wave = (uint32_t)wave_in_block();
   const uint32_t r = lane & 15u, h = lane >> 4;
-  const uint32_t units = a.route->units;
-  for (uint32_t j = threadIdx.x; j < a.most_units; j += kWave * kDownWaves) unit[j] = a.route->unit[j];
-  for (uint32_t j = threadIdx.x; j < a.tokens * a.top_k; j += kWave * kDownWaves) token[j] = a.route->token[j];
+  const uint32_t units = a.route->units, pairs = a.tokens * a.top_k;
+  for (uint32_t j = threadIdx.x; j < pairs; j += kWave * kDownWaves) {  // there are no more units than pairs
+    unit[j] = a.route->unit[j];
+    token[j] = a.route->token[j];
+  }
   float* const mine = ysum + wave * a.tokens * 16u;
   for (uint32_t j = threadIdx.x; j < kDownWaves * a.tokens * 4u; j += kWave * kDownWaves)
     ((mfma_f32x4*)ysum)[j] = mfma_f32x4{0, 0, 0, 0};
@@ -533,48 +591,75 @@ __global__ __launch_bounds__(kWave * kDownWaves) void k_moe_down(MoeArgs a) {
     u32x4 x[kB][4];
     uint32_t unit;
   };
-  auto use = [&](Slot& s) __attribute__((always_inline)) {
-    if (s.unit != now) {
-      flush();
-      now = s.unit;
-    }
-    quad_transpose(s.w.v);
-    each<kB>([&](auto j) __attribute__((always_inline)) {
-      each<4>([&](auto k) __attribute__((always_inline)) {
-        acc = mfma16(weight_operand<KIND>(s.w, j, k), s.x[j][k], acc);
-      });
-    });
-  };
+  const WeightLane<KIND> lw(a.inter);
   const uint32_t whole = a.inter / kStepCols<KIND>;
   const uint32_t per = a.act_blocks / kB;  // steps of a unit, a short last one among them
-  const uint32_t steps = units * per;
-  const uint32_t s0 = (uint32_t)((uint64_t)wave * steps / kDownWaves);
-  const uint32_t s1 = (uint32_t)((uint64_t)(wave + 1u) * steps / kDownWaves);
+  const uint32_t waves = a.parts * kDownWaves, at = blockIdx.y * kDownWaves + wave;
+  const uint32_t s0 = (uint32_t)((uint64_t)at * (units * per) / waves);
+  const uint32_t s1 = (uint32_t)((uint64_t)(at + 1u) * (units * per) / waves);
   uint32_t lu = s0 / per, ls = s0 - lu * per;  // the next step to load
   step_batches<U, Slot>(
       s1 - s0,
       [&](uint32_t, Slot& s) __attribute__((always_inline)) {
-        const uint64_t e = (uint32_t)__builtin_amdgcn_readfirstlane((int)unit[lu].expert);
-        const WeightTile<KIND> w(a.dn, a.dn_scales, e * a.hidden + row0, (e + 1u) * a.hidden, a.inter);
+        const MoeUnit un = unit[lu];
+        const uint64_t e = (uint32_t)__builtin_amdgcn_readfirstlane((int)un.expert);
+        const WeightTile<KIND> w(a.dn, a.dn_scales, e * a.hidden + row0, (uint64_t)a.experts * a.hidden, lw);
         if (ls < whole)
-          load_weights<KIND, false>(w, ls, s.w);
+          load_weights<KIND, false>(lw, w, ls, s.w);
         else
-          load_weights<KIND, true>(w, ls, s.w);
-        const u32x4* x = (const u32x4*)a.act + ((uint64_t)lu * a.act_blocks + ls * kB) * (4u * kWave) + lane;
-        each<4 * kB>([&](auto i) __attribute__((always_inline)) { s.x[i / 4][i % 4] = x[i * kWave]; });
+          load_weights<KIND, true>(lw, w, ls, s.w);
+        const uint32_t i = r & 7u, last = un.count - 1u;  // columns past the tokens repeat the last one
+        const u32x4* x = act_of(a, un) + 2u * (i < last ? i : last) + (r >> 3);
+        each<4 * kB>([&](auto q) __attribute__((always_inline)) {
+          s.x[q / 4][q % 4] = x[operand_at(ls * kB + q / 4, q % 4, h, 2u * un.count, 0)];
+        });
         s.unit = lu;
         const bool wrap = ls + 1u == per;
         lu += wrap ? 1u : 0u;
         ls = wrap ? 0u : ls + 1u;
       },
-      use);
+      [&](Slot& s) __attribute__((always_inline)) {
+        if (s.unit != now) {
+          flush();
+          now = s.unit;
+        }
+        quad_transpose(s.w.v);
+        each<kB>([&](auto j) __attribute__((always_inline)) {
+          each<4>([&](auto k) __attribute__((always_inline)) {
+            acc = mfma16(weight_operand<KIND>(s.w, j, k), s.x[j][k], acc);
+          });
+        });
+      });
   flush();
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < a.tokens * 16u; i += kWave * kDownWaves) {
+  const uint32_t n = a.tokens * 16u;
+  float* const parts = a.partial + (uint64_t)blockIdx.x * a.parts * n;
+  for (uint32_t i = threadIdx.x; i < n; i += kWave * kDownWaves) {
     float s = 0.0f;
-    for (uint32_t v = 0; v < kDownWaves; ++v) s += ysum[v * a.tokens * 16u + i];
-    const uint32_t t = i / 16u, o = row0 + i % 16u;
-    if (o < a.hidden) a.y[(uint64_t)t * a.hidden + o] = bf16_of(s);
+    for (uint32_t v = 0; v < kDownWaves; ++v) s += ysum[v * n + i];
+    if (a.parts == 1u) {
+      const uint32_t o = row0 + i % 16u;
+      if (o < a.hidden) a.y[(uint64_t)(i / 16u) * a.hidden + o] = bf16_of(s);
+    } else {
+      __hip_atomic_store(&parts[blockIdx.y * n + i], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  if (a.parts == 1u) return;
+  // The sums are stored and loaded as agent-scope atomics, which go past the
+  // caches that the card's dies do not share; a wait for the stores then orders
+  // them before the arrival.  (A fence would write back the whole L2: 85 us.)
+  wait_vm<0>();
+  __syncthreads();
+  if (threadIdx.x == 0)
+    before = __hip_atomic_fetch_add(&a.arrived[blockIdx.x], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (before + 1u != a.parts) return;
+  for (uint32_t i = threadIdx.x; i < n; i += kWave * kDownWaves) {
+    float s = 0.0f;
+    for (uint32_t v = 0; v < a.parts; ++v)
+      s += __hip_atomic_load(&parts[v * n + i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t o = row0 + i % 16u;
+    if (o < a.hidden) a.y[(uint64_t)(i / 16u) * a.hidden + o] = bf16_of(s);
   }
 }
 
@@ -587,6 +672,7 @@ int moe_shape_ok(const wc_moe_shape* s) {
   if (s->top_k < 1 || s->top_k > WC_MOE_MAX_TOP_K || s->top_k > s->experts) return WC_E_UNSUPPORTED;
   if (s->hidden < 1 || s->hidden > WC_MOE_MAX_DIM || s->inter < 1 || s->inter > WC_MOE_MAX_DIM)
     return WC_E_UNSUPPORTED;
+  static_assert(WC_MOE_MAX_DIM * 2u <= kUpInputs, "one token's inputs fit k_moe_gate_up's LDS");
   if (s->scoring > WC_MOE_SIGMOID || (s->flags & ~WC_MOE_RENORM)) return WC_E_ARG;
   return WC_OK;
 }
@@ -596,22 +682,6 @@ int experts_ok(const wc_moe_experts* e) {
   if (!e->d_data || !aligned16(e->d_data)) return WC_E_ARG;
   if (e->kind == WC_MOE_FP4 && !e->d_scales) return WC_E_ARG;
   return WC_OK;
-}
-
-template <int KIND, bool ANY>
-void launch_gate_up(const MoeArgs& a, uint32_t units, hipStream_t s) {
-  constexpr uint32_t kSplit = 4;
-  const dim3 block(kWave * kUpWaves);
-  const uint64_t items = (uint64_t)units * ((a.inter + 15u) / 16u);
-  const uint64_t most = (uint64_t)cu_count() * 3u;
-  auto blocks = [&](uint32_t per) {
-    const uint64_t b = (items + per - 1u) / per;
-    return (uint32_t)(b < most ? b : most);
-  };
-  if (a.tokens > 16u)
-    k_moe_gate_up<KIND, ANY, true, kSplit><<<blocks(kUpWaves / kSplit), block, 0, s>>>(a);
-  else
-    k_moe_gate_up<KIND, ANY, false, kSplit><<<blocks(kUpWaves / kSplit), block, 0, s>>>(a);
 }
 
 }  // namespace
@@ -659,33 +729,52 @@ extern "C" int wc_moe(const wc_moe_shape* shape, const uint16_t* d_x, const uint
   a.renorm = shape->flags & WC_MOE_RENORM;
   a.scale = shape->scale;
 
+  a.arrived = (uint32_t*)(work + m.arrived);
+  a.partial = (float*)(work + m.partial);
+  a.up_tokens = wc::moe_up_tokens(a.hidden);
+  a.down_fp4 = down->kind == WC_MOE_FP4;
+  a.act_blocks = wc::moe_blocks(a.inter, a.down_fp4 ? wc::kStepCols<wc::kFp4> : wc::kStepCols<wc::kBf16>);
+  const uint32_t row_blocks = (a.hidden + 15u) / 16u, cus = wc::cu_count();
+  a.parts = 1;
+  // rows too few for the card, and at least some steps for every wave
+  const uint64_t steps = (uint64_t)a.tokens * a.top_k * a.act_blocks / (a.down_fp4 ? 4u : 1u);
+  while (a.parts < wc::kMaxParts && 4u * row_blocks * a.parts < 3u * cus &&
+         steps >= 4u * wc::kDownWaves * a.parts)
+    a.parts *= 2u;
+
   const dim3 router_grid((a.experts + 15u) / 16u, (a.tokens + 15u) / 16u);
-  if (a.hidden % 8u)
+  const bool any = a.hidden % 8u != 0;  // rows that do not start at 16-byte boundaries
+  if (any)
     wc::k_moe_router<true><<<router_grid, wc::kWave * wc::kRouterWaves, 0, s>>>(a);
   else
     wc::k_moe_router<false><<<router_grid, wc::kWave * wc::kRouterWaves, 0, s>>>(a);
   if (hipGetLastError() != hipSuccess) return WC_E_HIP;
 
-  const uint32_t up_units = wc::moe_units(*shape, wc::kUpTokens);
-  a.most_units = wc::moe_units(*shape, wc::kDownTokens);
-  a.down_fp4 = down->kind == WC_MOE_FP4;
-  a.act_blocks = wc::moe_act_blocks(a.inter, a.down_fp4 ? wc::kStepCols<wc::kFp4> : wc::kStepCols<wc::kBf16>);
-  const bool any = a.hidden % 8u != 0;  // rows that do not start at 16-byte boundaries
+  // tiles there are at least when every pair has an expert of its own, or all share
+  const uint32_t pairs = a.tokens * a.top_k;
+  const uint64_t items = (uint64_t)pairs * ((a.inter + 15u) / 16u);
+  const uint32_t blocks = (uint32_t)(items < cus ? items : cus);
+  const uint32_t most = a.tokens < a.up_tokens ? a.tokens : a.up_tokens;
+  const size_t sums = (size_t)wc::kUpWaves * 4u * wc::kWave * sizeof(wc::mfma_f32x4);
+  const size_t in = (size_t)most * 256u *
+      wc::moe_blocks(a.hidden, gate_up->kind == WC_MOE_FP4 ? wc::kStepCols<wc::kFp4> : wc::kStepCols<wc::kBf16>);
+  const size_t lds_up = in > sums ? in : sums;
+  const dim3 up_block(wc::kWave * wc::kUpWaves);
   if (gate_up->kind == WC_MOE_FP4)
-    any ? wc::launch_gate_up<wc::kFp4, true>(a, up_units, s) : wc::launch_gate_up<wc::kFp4, false>(a, up_units, s);
+    wc::k_moe_gate_up<wc::kFp4, WC_DU><<<blocks, up_block, lds_up, s>>>(a);
+  else if (any)
+    wc::k_moe_gate_up<wc::kBf16Any, WC_DUB><<<blocks, up_block, lds_up, s>>>(a);
   else
-    any ? wc::launch_gate_up<wc::kBf16Any, true>(a, up_units, s)
-        : wc::launch_gate_up<wc::kBf16, false>(a, up_units, s);
+    wc::k_moe_gate_up<wc::kBf16, WC_DUB><<<blocks, up_block, lds_up, s>>>(a);
   if (hipGetLastError() != hipSuccess) return WC_E_HIP;
 
-  const uint32_t row_blocks = (a.hidden + 15u) / 16u;
   const size_t lds = (size_t)wc::kDownWaves * a.tokens * 16u * sizeof(float);
-  const dim3 block(wc::kWave * wc::kDownWaves);
-  if (down->kind == WC_MOE_FP4)
-    wc::k_moe_down<wc::kFp4, 1><<<row_blocks, block, lds, s>>>(a);
+  const dim3 block(wc::kWave * wc::kDownWaves), grid(row_blocks, a.parts);
+  if (a.down_fp4)
+    wc::k_moe_down<wc::kFp4, 1><<<grid, block, lds, s>>>(a);
   else if (a.inter % 8u)
-    wc::k_moe_down<wc::kBf16Any, 2><<<row_blocks, block, lds, s>>>(a);
+    wc::k_moe_down<wc::kBf16Any, 2><<<grid, block, lds, s>>>(a);
   else
-    wc::k_moe_down<wc::kBf16, 2><<<row_blocks, block, lds, s>>>(a);
+    wc::k_moe_down<wc::kBf16, 2><<<grid, block, lds, s>>>(a);
   return hipGetLastError() == hipSuccess ? WC_OK : WC_E_HIP;
 }

@@ -145,31 +145,37 @@ __device__ __forceinline__ void quad_transpose(u32x4 v[4]) {
 
 // ---- weights -----------------------------------------------------------------
 
-// 16 weight rows, row0 .. row0 + 15 of `rows` (those past the end repeat the last
-// one, and their sums are not used), seen by one lane.
+// Where a lane's pieces stand in a tile of 16 rows of `cols` columns: the same for
+// every tile of an array.
+template <int KIND>
+struct WeightLane {
+  uint32_t cols, row_bytes, groups;
+  uint32_t off[4];     // piece lane & 3 of row 4b + i
+  uint32_t scale_off;  // kFp4: of the lane's MFMA row r, from group 4 h on
+
+  __device__ __forceinline__ explicit WeightLane(uint32_t c) : cols(c) {
+    const uint32_t lane = (uint32_t)lane_id(), r = lane & 15u, h = lane >> 4;
+    groups = (uint32_t)WC_FP4_GROUPS(c);
+    row_bytes = KIND == kFp4 ? groups * 16u : c * 2u;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) off[i] = ((r & ~3u) + i) * row_bytes + 64u * h + 16u * (r & 3u);
+    scale_off = r * groups + 4u * h;
+  }
+};
+
+// Rows row0 .. row0 + 15 of an array of `rows` rows (all of it wave-uniform).
+// Sums of rows past the end come out as 0, or as another row's, and are not used.
 template <int KIND>
 struct WeightTile {
-  const uint8_t* data;  // of row0; wave-uniform
-  uint32_t bytes;
-  uint32_t off[4];        // the lane's piece of row 4b + i
-  const uint8_t* scales;  // kFp4: of the lane's MFMA row r, from group 4 h on
-  uint32_t cols;
+  const uint8_t* data;
+  const uint8_t* scales;
+  uint32_t n;  // rows that exist, up to 16
 
   __device__ __forceinline__ WeightTile(const void* d, const uint8_t* s, uint64_t row0, uint64_t rows,
-                                        uint32_t c)
-      : cols(c) {
-    const uint32_t lane = (uint32_t)lane_id(), r = lane & 15u, h = lane >> 4;
-    const uint32_t n = rows - row0 < 16u ? (uint32_t)(rows - row0) : 16u;
-    const uint32_t groups = (uint32_t)WC_FP4_GROUPS(c);
-    const uint32_t row_bytes = KIND == kFp4 ? groups * 16u : c * 2u;
-    data = (const uint8_t*)d + row0 * row_bytes;
-    bytes = n * row_bytes;
-#pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) {
-      const uint32_t q = (r & ~3u) + i;
-      off[i] = (q < n ? q : n - 1u) * row_bytes + 64u * h + 16u * (r & 3u);
-    }
-    if constexpr (KIND == kFp4) scales = s + (row0 + (r < n ? r : n - 1u)) * groups + 4u * h;
+                                        const WeightLane<KIND>& l) {
+    n = rows - row0 < 16u ? (uint32_t)(rows - row0) : 16u;
+    data = (const uint8_t*)d + row0 * l.row_bytes;
+    scales = KIND == kFp4 ? s + row0 * l.groups : nullptr;
   }
 };
 
@@ -181,35 +187,35 @@ struct WeightStep {
 
 // TAIL: the row's last step, of which some columns do not exist: they read as 0.
 template <int KIND, bool TAIL>
-__device__ __forceinline__ void load_weights(const WeightTile<KIND>& w, uint32_t step, WeightStep& s) {
-  const uint32_t lane = (uint32_t)lane_id(), h = lane >> 4, j = lane & 3u;
+__device__ __forceinline__ void load_weights(const WeightLane<KIND>& l, const WeightTile<KIND>& w,
+                                             uint32_t step, WeightStep& s) {
+  const uint32_t lane = (uint32_t)lane_id(), r = lane & 15u, h = lane >> 4, j = lane & 3u;
   if constexpr (KIND == kFp4) {
-    const buffer b = buffer_of(w.data, w.bytes);
-    const uint32_t groups = (uint32_t)WC_FP4_GROUPS(w.cols);
-    const bool in = !TAIL || step * 16u + 4u * h + j < groups;
+    const buffer b = buffer_of(w.data, w.n * l.row_bytes);  // rows past the end read as 0
+    const bool in = !TAIL || step * 16u + 4u * h + j < l.groups;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s.v[i] = load16(b, in ? w.off[i] : kNowhere, step * 256u);
+    for (int i = 0; i < 4; ++i) s.v[i] = load16(b, in ? l.off[i] : kNowhere, step * 256u);
+    const uint8_t* scales = w.scales + (r < w.n ? l.scale_off : 4u * h) + step * 16u;
     if constexpr (TAIL) {
       s.e = 0;
 #pragma unroll
       for (uint32_t k = 0; k < 4; ++k)
-        if (step * 16u + 4u * h + k < groups) s.e |= (uint32_t)w.scales[step * 16u + k] << (8u * k);
+        if (step * 16u + 4u * h + k < l.groups) s.e |= (uint32_t)scales[k] << (8u * k);
     } else {
-      s.e = *(const u32_any*)(w.scales + step * 16u);
+      s.e = *(const u32_any*)scales;
     }
   } else if constexpr (KIND == kBf16) {
-    const buffer b = buffer_of(w.data, w.bytes);
-    const bool in = !TAIL || step * 128u + 32u * h + 8u * j < w.cols;
+    const buffer b = buffer_of(w.data, w.n * l.row_bytes);
+    const bool in = !TAIL || step * 128u + 32u * h + 8u * j < l.cols;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s.v[i] = load16(b, in ? w.off[i] : kNowhere, step * 256u);
+    for (int i = 0; i < 4; ++i) s.v[i] = load16(b, in ? l.off[i] : kNowhere, step * 256u);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint8_t* p = w.data + w.off[i];
-      if constexpr (TAIL)
-        s.v[i] = load8((const uint16_t*)(p - 64u * h - 16u * j), step * 128u + 32u * h + 8u * j, w.cols);
-      else
-        s.v[i] = *(const u32x4_any*)(p + (size_t)step * 256u);
+    for (uint32_t i = 0; i < 4; ++i) {
+      const uint32_t q = (r & ~3u) + i;
+      const uint16_t* row = (const uint16_t*)(w.data + (uint64_t)(q < w.n ? q : w.n - 1u) * l.row_bytes);
+      const uint32_t c = step * 128u + 32u * h + 8u * j;
+      s.v[i] = TAIL ? load8(row, c, l.cols) : *(const u32x4_any*)(row + c);
     }
   }
 }

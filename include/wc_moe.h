@@ -43,7 +43,7 @@ extern "C" {
 #define WC_MOE_MAX_TOKENS 64u
 #define WC_MOE_MAX_EXPERTS 512u
 #define WC_MOE_MAX_TOP_K 16u
-#define WC_MOE_MAX_DIM (1u << 18) /* hidden and inter */
+#define WC_MOE_MAX_DIM 65536u /* hidden and inter */
 
 typedef struct wc_moe_shape {
   uint32_t tokens;  /* 1..WC_MOE_MAX_TOKENS, else WC_E_UNSUPPORTED */

@@ -275,7 +275,7 @@ def _moe_call(shape=(3, 64, 40, 5, 2, 0, 1, 1.0), x=64, router=64, bias=None, gu
     (dict(shape=None), -1), (dict(gu=None), -1), (dict(dn=None), -1),
     (dict(shape=(0, 64, 40, 5, 2, 0, 1, 1.0)), -5), (dict(shape=(65, 64, 40, 5, 2, 0, 1, 1.0)), -5),
     (dict(shape=(3, 0, 40, 5, 2, 0, 1, 1.0)), -5), (dict(shape=(3, 64, 0, 5, 2, 0, 1, 1.0)), -5),
-    (dict(shape=(3, (1 << 18) + 1, 40, 5, 2, 0, 1, 1.0)), -5),
+    (dict(shape=(3, 65537, 40, 5, 2, 0, 1, 1.0)), -5),
     (dict(shape=(3, 64, 40, 0, 0, 0, 1, 1.0)), -5), (dict(shape=(3, 64, 40, 513, 2, 0, 1, 1.0)), -5),
     (dict(shape=(3, 64, 40, 5, 6, 0, 1, 1.0)), -5), (dict(shape=(3, 64, 40, 32, 17, 0, 1, 1.0)), -5),
     (dict(shape=(3, 64, 40, 5, 2, 2, 1, 1.0)), -1), (dict(shape=(3, 64, 40, 5, 2, 0, 2, 1.0)), -1),

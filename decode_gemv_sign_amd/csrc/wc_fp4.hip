@@ -304,6 +304,11 @@ void launch_wide(const Fp4Args& a, hipStream_t s) {
                            in > sums ? in : sums, s>>>(a);
 }
 
+// At up to 16 input rows: blocks of 32 rows, two per compute unit (24576 x 6144,
+// batch 16: 27.0 -> 23.5 us; below that 16 rows and no LDS are faster: 4096 x 4096
+// 5.2 against 7.1).
+bool tall_enough(const Fp4Args& a) { return a.rows >= 32u * (cu_count() * 5u / 4u); }
+
 // Every block reads the inputs of its batch tiles whole, so the tallest tile whose
 // blocks still fill the compute units is the fastest (6144 x 24576, batch 64: 64
 // rows 73.7 us, 32 rows 58.6; 14336 x 4096: 22.3, 28.4; 4096 x 4096 at two
@@ -314,7 +319,9 @@ void launch_wide_for(const Fp4Args& a, hipStream_t s) {
     return (a.rows + 16u * mt - 1u) / (16u * mt) * ((a.batch + 16u * nt - 1u) / (16u * nt));
   };
   const uint64_t enough = cu_count() * 5u / 8u;
-  if (a.batch > 32 && blocks(4, 4) >= enough)
+  if (a.batch <= 16)
+    launch_wide<2, 1, 4>(a, s);
+  else if (a.batch > 32 && blocks(4, 4) >= enough)
     launch_wide<4, 4, 4>(a, s);
   else if (a.batch > 32 && blocks(2, 4) >= enough)
     launch_wide<2, 4, 4>(a, s);
@@ -374,7 +381,7 @@ extern "C" int wc_fp4_gemv(const uint8_t* d_codes, const uint8_t* d_scales, uint
   const uint32_t rb = (uint32_t)row_blocks;
   if (batch <= 4)
     wc::launch_rows<true>(a, rb, 1, s);
-  else if (batch <= 16 || cols % 8u)
+  else if (cols % 8u || (batch <= 16 && !wc::tall_enough(a)))
     wc::launch_rows<false>(a, rb, (batch + 15u) / 16u, s);
   else
     wc::launch_wide_for(a, s);

@@ -15,17 +15,13 @@
 #include "wc_moe.h"
 #include "wc_skinny.h"
 
-#ifndef WC_DU
-#define WC_DU 1
-#define WC_DUB 2
-#endif
-
 namespace wc {
 
 constexpr uint32_t kMoeExperts = WC_MOE_MAX_EXPERTS;
 constexpr uint32_t kMoePlaces = WC_MOE_MAX_TOKENS * WC_MOE_MAX_TOP_K;  // (token, choice) pairs
-constexpr uint32_t kRouterWaves = 16;
-constexpr uint32_t kUpWaves = 16;    // waves per block of k_moe_gate_up, one block per compute unit
+constexpr uint32_t kRouterWaves = 8;
+constexpr uint32_t kMaxSplits = 4;   // column splits of the router
+constexpr uint32_t kUpWaves = 12;    // waves per block of k_moe_gate_up, one block per compute unit
 constexpr uint32_t kDownWaves = 16;  // and of k_moe_down
 constexpr uint32_t kMaxParts = 4;    // blocks of k_moe_down on the same rows
 
@@ -59,13 +55,15 @@ struct MoeArgs {
   uint16_t* y;
   int32_t* ids;
   float* weights;
-  float* logits;      // [tokens][experts]
+  float* logits;      // [splits][tokens][experts]: sums over a split of the columns
   MoeRoute* route;
   uint16_t* act;      // operands of k_moe_down (act_at below)
   uint32_t* arrived;  // blocks of k_moe_down that are done, by row tile
   float* partial;     // their sums, [row tile][part][tokens][16]
   uint32_t tokens, hidden, inter, experts, top_k, scoring, renorm;
+  uint32_t splits;      // of the router's columns
   uint32_t up_tokens;   // most tokens of a unit of k_moe_gate_up
+  uint32_t up_inputs;   // tokens whose inputs its LDS holds
   uint32_t act_blocks;  // of 128 columns per unit: inter rounded up to whole steps, the rest 0
   uint32_t down_fp4;    // the order of the columns in a step
   uint32_t parts;       // blocks of k_moe_down on the same rows
@@ -91,7 +89,7 @@ inline MoeWork moe_work(const wc_moe_shape& s) {
   MoeWork m;
   const uint64_t tiles = (s.hidden + 15u) / 16u;
   m.logits = 0;
-  m.route = pad16(m.logits + 4ull * s.tokens * s.experts);
+  m.route = pad16(m.logits + 4ull * kMaxSplits * s.tokens * s.experts);
   m.act = pad16(m.route + sizeof(MoeRoute));
   // 512 bytes a pair and block; whole 4-bit steps, so that the size does not go by the kind
   m.arrived = m.act + 512ull * s.tokens * s.top_k * moe_blocks(s.inter, kStepCols<kFp4>);
@@ -125,7 +123,7 @@ __device__ __forceinline__ u32x4* act_of(const MoeArgs& a, const MoeUnit& u) {
 
 // ---- router ------------------------------------------------------------------
 
-// Block = 16 experts x 16 tokens, a run of steps per wave.
+// Block = 16 experts x 16 tokens x a split of the columns, a run of steps per wave.
 template <bool ANY>
 __global__ __launch_bounds__(kWave * kRouterWaves) void k_moe_router(MoeArgs a) {
   __shared__ mfma_f32x4 part[kRouterWaves][kWave];
@@ -133,10 +131,10 @@ __global__ __launch_bounds__(kWave * kRouterWaves) void k_moe_router(MoeArgs a) 
   const uint32_t r = lane & 15u;
   const uint32_t e0 = blockIdx.x * kRowTile, t0 = blockIdx.y * kRowTile;
   // the counters that k_moe_down's blocks count in
-  const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x;
-  for (uint32_t i = block * (kWave * kRouterWaves) + threadIdx.x; i < (a.hidden + 15u) / 16u;
-       i += gridDim.x * gridDim.y * (kWave * kRouterWaves))
-    a.arrived[i] = 0;
+  if (blockIdx.y == 0 && blockIdx.z == 0)
+    for (uint32_t i = blockIdx.x * (kWave * kRouterWaves) + threadIdx.x; i < (a.hidden + 15u) / 16u;
+         i += gridDim.x * (kWave * kRouterWaves))
+      a.arrived[i] = 0;
   constexpr int kKind = ANY ? kBf16Any : kBf16;
   const WeightLane<kKind> lw(a.hidden);
   const WeightTile<kKind> w(a.router, nullptr, e0, a.experts, lw);
@@ -154,7 +152,8 @@ __global__ __launch_bounds__(kWave * kRouterWaves) void k_moe_router(MoeArgs a) 
     for (int k = 0; k < 4; ++k) acc = mfma16(s.w.v[k], s.x.v[k], acc);
   };
   const uint32_t whole = a.hidden / kStepCols<kKind>;
-  const uint32_t s0 = wave * whole / kRouterWaves, s1 = (wave + 1u) * whole / kRouterWaves;
+  const uint32_t at = blockIdx.z * kRouterWaves + wave, waves = a.splits * kRouterWaves;
+  const uint32_t s0 = at * whole / waves, s1 = (at + 1u) * whole / waves;
   step_batches<2, Slot>(
       s1 - s0,
       [&](uint32_t q, Slot& s) __attribute__((always_inline)) {
@@ -162,7 +161,7 @@ __global__ __launch_bounds__(kWave * kRouterWaves) void k_moe_router(MoeArgs a) 
         load_inputs<kKind, false>(x, s0 + q, 0, s.x);
       },
       use);
-  if (wave == kRouterWaves - 1u && whole * kStepCols<kKind> < a.hidden) {
+  if (at == waves - 1u && whole * kStepCols<kKind> < a.hidden) {
     Slot s;
     load_weights<kKind, true>(lw, w, whole, s.w);
     load_inputs<kKind, true>(x, whole, 0, s.x);
@@ -175,7 +174,7 @@ __global__ __launch_bounds__(kWave * kRouterWaves) void k_moe_router(MoeArgs a) 
 #pragma unroll
     for (int v = 1; v < kRouterWaves; ++v) s += part[v][lane];
     if (t0 + r < a.tokens) {
-      float* o = a.logits + (uint64_t)(t0 + r) * a.experts;
+      float* o = a.logits + ((uint64_t)blockIdx.z * a.tokens + t0 + r) * a.experts;
 #pragma unroll
       for (uint32_t k = 0; k < 4; ++k) {
         const uint32_t ee = e0 + 4u * (lane >> 4) + k;
@@ -250,11 +249,21 @@ __device__ inline void choose(const MoeArgs& a, uint32_t t, MoeChoice& c) {
   constexpr uint32_t kLanes = WIDE ? 64u : 16u;
   const uint32_t r = (uint32_t)lane_id() & (kLanes - 1u);
   const bool real = t < a.tokens;
-  const float* row = a.logits + (uint64_t)(real ? t : 0u) * a.experts;
-  float logit[PER], score[PER];
+  float logit[PER], score[PER], more[kMaxSplits][PER];
   uint32_t key[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) logit[i] = row[r + kLanes * i < a.experts ? r + kLanes * i : 0u];
+  for (uint32_t s = 0; s < kMaxSplits; ++s) {  // all loads together
+    const float* row = a.logits + ((uint64_t)(s < a.splits ? s : 0u) * a.tokens + (real ? t : 0u)) * a.experts;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) more[s][i] = row[r + kLanes * i < a.experts ? r + kLanes * i : 0u];
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    logit[i] = more[0][i];
+#pragma unroll
+    for (uint32_t s = 1; s < kMaxSplits; ++s)
+      if (s < a.splits) logit[i] += more[s][i];
+  }
   if (a.scoring == WC_MOE_SOFTMAX) {
     uint32_t top = 0;
 #pragma unroll
@@ -387,12 +396,13 @@ __device__ inline void choose_all(const MoeArgs& a, MoeChoice& c, MoeRoute* rout
 // ---- gate and up ---------------------------------------------------------------
 
 // A block's share of the tiles (unit, 16 rows of gate and the same 16 of up) is
-// one run of them, unit by unit.  The inputs of a unit's tokens come to LDS in
-// operand order; then the steps of all the block's tiles of that unit, tile by
-// tile, are shared out evenly: each wave takes one run of steps, and a tile that
-// several waves worked on is joined in LDS, in wave order.
-template <int KIND, int U>
-__global__ __launch_bounds__(kWave * kUpWaves) void k_moe_gate_up(MoeArgs a) {
+// one run of them, unit by unit, which it takes in as few parts as the inputs of
+// their tokens fit LDS, mostly one.  The inputs come there in operand order; then
+// the steps of all the part's tiles are shared out evenly: each wave takes one run
+// of steps, and a tile that several waves worked on is joined in LDS, in wave
+// order.
+template <int KIND>
+__global__ __launch_bounds__(kWave * kUpWaves, 3) void k_moe_gate_up(MoeArgs a) {
   __shared__ MoeChoice c;
   extern __shared__ __attribute__((aligned(16))) u32x4 inputs[];  // then sums[kUpWaves][2][2][kWave]
   mfma_f32x4* const sums = (mfma_f32x4*)inputs;
@@ -405,7 +415,7 @@ __global__ __launch_bounds__(kWave * kUpWaves) void k_moe_gate_up(MoeArgs a) {
   const uint32_t whole = a.hidden / kStepCols<KIND>;
   const uint32_t steps = (a.hidden + kStepCols<KIND> - 1u) / kStepCols<KIND>;
   const WeightLane<KIND> lw(a.hidden);
-  const uint32_t end = (uint32_t)((uint64_t)(blockIdx.x + 1u) * items / gridDim.x);
+  const uint32_t end = (blockIdx.x + 1u) * items / gridDim.x;
 
   // The tile's sums g and u, for the unit's tokens: into act.
   auto finish = [&](const MoeUnit& unit, uint32_t tile, mfma_f32x4 g, mfma_f32x4 u) __attribute__((always_inline)) {
@@ -437,75 +447,97 @@ __global__ __launch_bounds__(kWave * kUpWaves) void k_moe_gate_up(MoeArgs a) {
       for (uint32_t i = i0 + kRowTile; i < a.act_blocks * 128u; i += kRowTile) put(i, uint2{0, 0}, uint2{0, 0});
   };
 
-  for (uint32_t item = (uint32_t)((uint64_t)blockIdx.x * items / gridDim.x); item < end;) {
-    const uint32_t un = item / tiles, tile0 = item - un * tiles;
-    const uint32_t count = end - item < tiles - tile0 ? end - item : tiles - tile0;  // tiles of the run
-    item += count;
-    const MoeUnit unit = c.unit[un];
-    // inputs, as [block][k][h][token]
-    const uint32_t pieces = steps * kB * 16u;
-    for (uint32_t i = threadIdx.x; i < pieces * unit.count; i += kWave * kUpWaves) {
-      const uint32_t t = i / pieces, q = i - t * pieces;
-      const uint16_t* row = a.x + (uint64_t)c.place_token[unit.place + t] * a.hidden;
-      const Piece p = piece_of<kIsFp4>(q);
-      inputs[operand_at(p.block, p.k, p.h, unit.count, t)] =
-          8u * q + 8u <= a.hidden ? *(const u32x4_any*)(row + 8u * q) : load8(row, 8u * q, a.hidden);
-    }
-    __syncthreads();
-    const uint32_t total = count * steps;
+  for (uint32_t item = blockIdx.x * items / gridDim.x; item < end;) {
+    const uint32_t item0 = item, unit0 = item0 / tiles, place0 = c.unit[unit0].place;
+    uint32_t unit1 = unit0 + 1u;  // the part's units: all that the block has, or that fit
+    while (unit1 * tiles < end && c.unit[unit1].place + c.unit[unit1].count - place0 <= a.up_inputs) ++unit1;
+    item = end < unit1 * tiles ? end : unit1 * tiles;
+    const uint32_t total = (item - item0) * steps;
     const uint32_t f0 = wave * total / kUpWaves, f1 = (wave + 1u) * total / kUpWaves;
-    const uint64_t gate = (uint64_t)unit.expert * 2u * a.inter, rows = (uint64_t)a.experts * 2u * a.inter;
-    const uint32_t mine = r < unit.count ? r : unit.count - 1u;  // columns past the tokens repeat the last one
+    const uint64_t rows = (uint64_t)a.experts * 2u * a.inter;
+    const uint32_t pieces = steps * kB * 16u;  // of a token's inputs
     mfma_f32x4 g = {0, 0, 0, 0}, u = {0, 0, 0, 0};
     mfma_f32x4 g0 = g, u0 = u;  // of the wave's first tile, when it is not the last
     uint32_t done = 0;          // whether that is so
-    uint32_t lt = f0 / steps, ls = f0 - lt * steps;  // the next step to load: tile, step
-    uint32_t ut = lt, us = ls;                       // and to use
+    // the next step to load: unit, tile, step; and to use
+    const uint32_t first = item0 + f0 / steps;
+    uint32_t lu = first / tiles, lt = first - lu * tiles, ls = f0 % steps;
+    uint32_t uu = lu, ut = lt, us = ls;
     const bool starts = ls == 0;  // the first tile has no steps before this wave
+    auto advance = [&](uint32_t& unit, uint32_t& tile, uint32_t& step) __attribute__((always_inline)) {
+      if (++step < steps) return;
+      step = 0;
+      if (++tile < tiles) return;
+      tile = 0;
+      ++unit;
+    };
     struct Slot {
       WeightStep g, u;
     };
-    step_batches<U, Slot>(
-        f1 - f0,
-        [&](uint32_t, Slot& s) __attribute__((always_inline)) {
-          const uint64_t row = (uint64_t)(tile0 + lt) * kRowTile;
-          const WeightTile<KIND> wg(a.gu, a.gu_scales, gate + row, rows, lw);
-          const WeightTile<KIND> wu(a.gu, a.gu_scales, gate + a.inter + row, rows, lw);
-          if (ls < whole) {
-            load_weights<KIND, false>(lw, wg, ls, s.g);
-            load_weights<KIND, false>(lw, wu, ls, s.u);
-          } else {
-            load_weights<KIND, true>(lw, wg, ls, s.g);
-            load_weights<KIND, true>(lw, wu, ls, s.u);
-          }
-          if (++ls == steps) {
-            ls = 0;
-            ++lt;
-          }
-        },
-        [&](Slot& s) __attribute__((always_inline)) {
-          quad_transpose(s.g.v);
-          quad_transpose(s.u.v);
-          each<kB>([&](auto j) __attribute__((always_inline)) {
-            each<4>([&](auto k) __attribute__((always_inline)) {
-              const u32x4 x = inputs[operand_at(us * kB + j, k, h, unit.count, mine)];
-              g = mfma16(weight_operand<KIND>(s.g, j, k), x, g);
-              u = mfma16(weight_operand<KIND>(s.u, j, k), x, u);
-            });
-          });
-          if (++us == steps) {  // the tile's last step
-            if (starts || done) {
-              finish(unit, tile0 + ut, g, u);
-            } else {
-              g0 = g;
-              u0 = u;
-            }
-            done = 1;
-            us = 0;
-            ++ut;
-            g = u = mfma_f32x4{0, 0, 0, 0};
-          }
+    auto load = [&](Slot& s) __attribute__((always_inline)) {
+      const uint64_t e = (uint32_t)__builtin_amdgcn_readfirstlane((int)c.unit[lu].expert);
+      const uint64_t row = e * 2u * a.inter + lt * kRowTile;
+      const WeightTile<KIND> wg(a.gu, a.gu_scales, row, rows, lw);
+      const WeightTile<KIND> wu(a.gu, a.gu_scales, row + a.inter, rows, lw);
+      if (ls < whole) {
+        load_weights<KIND, false>(lw, wg, ls, s.g);
+        load_weights<KIND, false>(lw, wu, ls, s.u);
+      } else {
+        load_weights<KIND, true>(lw, wg, ls, s.g);
+        load_weights<KIND, true>(lw, wu, ls, s.u);
+      }
+      advance(lu, lt, ls);
+    };
+    auto use = [&](Slot& s) __attribute__((always_inline)) {
+      const MoeUnit unit = c.unit[uu];
+      const u32x4* in = inputs + (unit.place - place0) * pieces;
+      const uint32_t mine = r < unit.count ? r : unit.count - 1u;  // columns past the tokens repeat the last one
+      quad_transpose(s.g.v);
+      quad_transpose(s.u.v);
+      each<kB>([&](auto j) __attribute__((always_inline)) {
+        each<4>([&](auto k) __attribute__((always_inline)) {
+          const u32x4 x = in[operand_at(us * kB + j, k, h, unit.count, mine)];
+          g = mfma16(weight_operand<KIND>(s.g, j, k), x, g);
+          u = mfma16(weight_operand<KIND>(s.u, j, k), x, u);
         });
+      });
+      if (us + 1u == steps) {  // the tile's last step
+        if (starts || done) {
+          finish(unit, ut, g, u);
+        } else {
+          g0 = g;
+          u0 = u;
+        }
+        done = 1;
+        g = u = mfma_f32x4{0, 0, 0, 0};
+      }
+      advance(uu, ut, us);
+    };
+    Slot now, next;
+    if (f0 < f1) load(now);  // on its way while the inputs come in
+    // inputs, unit by unit as [block][k][h][token]
+    for (uint32_t un = unit0; un < unit1; ++un) {
+      const MoeUnit unit = c.unit[un];
+      u32x4* in = inputs + (unit.place - place0) * pieces;
+      for (uint32_t i = threadIdx.x; i < pieces * unit.count; i += kWave * kUpWaves) {
+        const uint32_t t = i / pieces, q = i - t * pieces;
+        const uint16_t* row = a.x + (uint64_t)c.place_token[unit.place + t] * a.hidden;
+        const Piece p = piece_of<kIsFp4>(q);
+        in[operand_at(p.block, p.k, p.h, unit.count, t)] =
+            8u * q + 8u <= a.hidden ? *(const u32x4_any*)(row + 8u * q) : load8(row, 8u * q, a.hidden);
+      }
+    }
+    __syncthreads();
+    if (f0 < f1) {
+      // a step is loaded while the one before it is used
+      for (uint32_t f = f0 + 1u; f < f1; ++f) {
+        load(next);
+        __builtin_amdgcn_sched_barrier(0);
+        use(now);
+        now = next;
+      }
+      use(now);
+    }
     // Tiles shared with other waves: sums[wave][0] is the wave's part of its first
     // tile, [1] of its last one.  Tile t's steps t * steps .. are those of waves
     // w0 .. w1, and w1 joins them.
@@ -536,7 +568,8 @@ __global__ __launch_bounds__(kWave * kUpWaves) void k_moe_gate_up(MoeArgs a) {
         sg += sums[(v * 4u + slot) * kWave + lane];
         su += sums[(v * 4u + slot + 1u) * kWave + lane];
       }
-      finish(unit, tile0 + t, sg, su);
+      const uint32_t un = (item0 + t) / tiles;
+      finish(c.unit[un], item0 + t - un * tiles, sg, su);
     }
     __syncthreads();
   }
@@ -595,8 +628,8 @@ __global__ __launch_bounds__(kWave * kDownWaves) void k_moe_down(MoeArgs a) {
   const uint32_t whole = a.inter / kStepCols<KIND>;
   const uint32_t per = a.act_blocks / kB;  // steps of a unit, a short last one among them
   const uint32_t waves = a.parts * kDownWaves, at = blockIdx.y * kDownWaves + wave;
-  const uint32_t s0 = (uint32_t)((uint64_t)at * (units * per) / waves);
-  const uint32_t s1 = (uint32_t)((uint64_t)(at + 1u) * (units * per) / waves);
+  const uint32_t s0 = at * (units * per) / waves;
+  const uint32_t s1 = (at + 1u) * (units * per) / waves;
   uint32_t lu = s0 / per, ls = s0 - lu * per;  // the next step to load
   step_batches<U, Slot>(
       s1 - s0,
@@ -672,7 +705,7 @@ int moe_shape_ok(const wc_moe_shape* s) {
   if (s->top_k < 1 || s->top_k > WC_MOE_MAX_TOP_K || s->top_k > s->experts) return WC_E_UNSUPPORTED;
   if (s->hidden < 1 || s->hidden > WC_MOE_MAX_DIM || s->inter < 1 || s->inter > WC_MOE_MAX_DIM)
     return WC_E_UNSUPPORTED;
-  static_assert(WC_MOE_MAX_DIM * 2u <= kUpInputs, "one token's inputs fit k_moe_gate_up's LDS");
+  static_assert(WC_MOE_MAX_DIM * 2u <= 128u * 1024u, "one token's inputs fit k_moe_gate_up's LDS");
   if (s->scoring > WC_MOE_SIGMOID || (s->flags & ~WC_MOE_RENORM)) return WC_E_ARG;
   return WC_OK;
 }
@@ -742,7 +775,11 @@ extern "C" int wc_moe(const wc_moe_shape* shape, const uint16_t* d_x, const uint
          steps >= 4u * wc::kDownWaves * a.parts)
     a.parts *= 2u;
 
-  const dim3 router_grid((a.experts + 15u) / 16u, (a.tokens + 15u) / 16u);
+  // one step per wave up to 4096 columns: the router is small, its loads should go out together
+  const uint32_t router_steps = (a.hidden + 127u) / 128u;
+  a.splits = (router_steps + wc::kRouterWaves - 1u) / wc::kRouterWaves;
+  if (a.splits > wc::kMaxSplits) a.splits = wc::kMaxSplits;
+  const dim3 router_grid((a.experts + 15u) / 16u, (a.tokens + 15u) / 16u, a.splits);
   const bool any = a.hidden % 8u != 0;  // rows that do not start at 16-byte boundaries
   if (any)
     wc::k_moe_router<true><<<router_grid, wc::kWave * wc::kRouterWaves, 0, s>>>(a);
@@ -754,18 +791,20 @@ extern "C" int wc_moe(const wc_moe_shape* shape, const uint16_t* d_x, const uint
   const uint32_t pairs = a.tokens * a.top_k;
   const uint64_t items = (uint64_t)pairs * ((a.inter + 15u) / 16u);
   const uint32_t blocks = (uint32_t)(items < cus ? items : cus);
-  const uint32_t most = a.tokens < a.up_tokens ? a.tokens : a.up_tokens;
   const size_t sums = (size_t)wc::kUpWaves * 4u * wc::kWave * sizeof(wc::mfma_f32x4);
-  const size_t in = (size_t)most * 256u *
+  const uint32_t token_bytes = 256u *
       wc::moe_blocks(a.hidden, gate_up->kind == WC_MOE_FP4 ? wc::kStepCols<wc::kFp4> : wc::kStepCols<wc::kBf16>);
+  a.up_inputs = wc::kUpInputs / token_bytes;
+  if (a.up_inputs > pairs) a.up_inputs = pairs;
+  const size_t in = (size_t)a.up_inputs * token_bytes;
   const size_t lds_up = in > sums ? in : sums;
   const dim3 up_block(wc::kWave * wc::kUpWaves);
   if (gate_up->kind == WC_MOE_FP4)
-    wc::k_moe_gate_up<wc::kFp4, WC_DU><<<blocks, up_block, lds_up, s>>>(a);
+    wc::k_moe_gate_up<wc::kFp4><<<blocks, up_block, lds_up, s>>>(a);
   else if (any)
-    wc::k_moe_gate_up<wc::kBf16Any, WC_DUB><<<blocks, up_block, lds_up, s>>>(a);
+    wc::k_moe_gate_up<wc::kBf16Any><<<blocks, up_block, lds_up, s>>>(a);
   else
-    wc::k_moe_gate_up<wc::kBf16, WC_DUB><<<blocks, up_block, lds_up, s>>>(a);
+    wc::k_moe_gate_up<wc::kBf16><<<blocks, up_block, lds_up, s>>>(a);
   if (hipGetLastError() != hipSuccess) return WC_E_HIP;
 
   const size_t lds = (size_t)wc::kDownWaves * a.tokens * 16u * sizeof(float);

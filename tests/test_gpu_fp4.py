@@ -136,6 +136,15 @@ def test_gemv_at_ordinary_sizes(rows, cols, batch):
     check_gemv(rows, cols, batch)
 
 
+@pytest.mark.parametrize("rows,cols,batch", [(10300, 1000, 9), (10241, 512, 16), (10270, 8, 5), (10300, 520, 20),
+                                             (10250, 520, 40), (2600, 1056, 250), (5130, 1032, 50),
+                                             (5200, 648, 31), (10241, 100, 64)])
+def test_gemv_of_tall_matrices(rows, cols, batch):
+    """Rows and batches at which each of the taller blocks is taken, with a last
+    one that is not whole."""
+    check_gemv(rows, cols, batch)
+
+
 def test_gemv_integers_are_exact():
     """Sums of small whole numbers are exact in fp32 whatever their order."""
     rng = np.random.default_rng(5)

@@ -119,6 +119,21 @@ def test_all_tokens_choose_the_same_experts():
         assert bool(((ids == 2) | (ids == 7)).all())
 
 
+@pytest.mark.parametrize("T,H,I,k", [(9, 20000, 20, 2), (4, 65536, 8, 1), (64, 8200, 24, 2), (33, 4104, 72, 3),
+                                     (1, 12000, 40, 1)])
+@pytest.mark.parametrize("kinds", [("bf16", "bf16"), ("fp4", "fp4")])
+def test_wide_inputs(T, H, I, k, kinds):
+    """Inputs of which only some tokens' fit the LDS of a block at a time."""
+    check(Layer(T, H, I, 3, kinds, seed=30), k)
+
+
+@pytest.mark.parametrize("T,H,I", [(64, 96, 700), (30, 520, 1300), (8, 40, 4100), (64, 5000, 48)])
+@pytest.mark.parametrize("kinds", [("bf16", "bf16"), ("fp4", "fp4"), ("fp4", "bf16"), ("bf16", "fp4")])
+def test_long_second_products(T, H, I, kinds):
+    """Few and many output rows, each with a long sum over the chosen experts."""
+    check(Layer(T, H, I, 8, kinds, seed=30), 4)
+
+
 def test_ties_go_to_the_lowest_index():
     layer = Layer(6, 160, 32, 70, seed=7)
     layer.router[:] = layer.router[3]  # every logit of a token is the same

@@ -173,92 +173,126 @@ __global__ __launch_bounds__(kWave * 16) void k_fp4_gemv(Fp4Args a) {
 // at a time in different banks.  Nothing is shared between waves until the end,
 // so there is no barrier for their loads to wait at.
 constexpr uint32_t kWideLoad = 1024u + 16u;
-template <int MT, int NT, int KG>
-__global__ __launch_bounds__(kWave * KG) void k_fp4_wide(Fp4Args a) {
+constexpr uint32_t kWideWaves = 4;
+
+// Loads before it are issued before loads after it.
+__device__ __forceinline__ void load_fence() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <int MT, int NT, int D>
+__global__ __launch_bounds__(kWave * kWideWaves) void k_fp4_wide(Fp4Args a) {
   constexpr uint32_t kBuf = NT * 4u * kWideLoad;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // [KG][2][kBuf], then the sums
+  constexpr int kCodeLoads = 5;  // of a step of a tile: four of codes, one of scales
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // [kWideWaves][D][kBuf], then the sums
   const uint32_t lane = (uint32_t)lane_id(), kg = (uint32_t)wave_in_block();
   const uint32_t r = lane & 15u, h = lane >> 4;
   const uint64_t row0 = (uint64_t)blockIdx.x * (kRowTile * MT);
   const uint32_t b0 = blockIdx.y * (kRowTile * NT);
-  uint8_t* const mine = lds + kg * (2u * kBuf);
+  uint8_t* const mine = lds + kg * (D * kBuf);
   const uint32_t steps = (a.cols + kStepCols<kFp4> - 1u) / kStepCols<kFp4>;
   const uint32_t whole = a.cols / kStepCols<kFp4>;
-  const uint32_t s0 = kg * steps / KG, s1 = (kg + 1u) * steps / KG;
-  // the lane's input rows
-  const uint16_t* x[NT * 4];
+  const uint32_t s0 = kg * steps / kWideWaves, s1 = (kg + 1u) * steps / kWideWaves;
+  // the lane's places in the inputs: at most 64 rows of 32 MiB
+  const uint32_t nb = a.batch - b0 < NT * 16u ? a.batch - b0 : NT * 16u;
+  const uint16_t* const x0 = a.x + (uint64_t)b0 * a.cols;
+  const uint32_t c0 = 128u * h + 8u * (lane & 3u);
+  uint32_t x[NT * 4];  // in bytes
   each<NT * 4>([&](auto i) __attribute__((always_inline)) {
-    const uint32_t b = b0 + (i / 4u) * 16u + (r & ~3u) + i % 4u;
-    x[i] = a.x + (uint64_t)(b < a.batch ? b : a.batch - 1u) * a.cols;
+    const uint32_t b = (i / 4u) * 16u + (r & ~3u) + i % 4u;
+    x[i] = ((b < nb ? b : nb - 1u) * a.cols + c0) * 2u;
   });
-  auto stage = [&](uint32_t s, auto j, uint32_t buf) __attribute__((always_inline)) {
-    const uint32_t c = s * kStepCols<kFp4> + 128u * h + 32u * j + 8u * (lane & 3u);
-    uint8_t* const to = mine + buf * kBuf;
-    if (s < whole) {
-      each<NT * 4>([&](auto i) __attribute__((always_inline)) {
-        lds_dma16_keep(x[i] + c, (uint32_t*)(to + i * kWideLoad));
-      });
-    } else {  // cols is a multiple of 8: a piece is in or out
-      each<NT * 4>([&](auto i) __attribute__((always_inline)) {
-        *(u32x4*)(to + i * kWideLoad + 16u * lane) = c < a.cols ? *(const u32x4*)(x[i] + c) : u32x4{0, 0, 0, 0};
-      });
-    }
+  auto stage = [&](uint32_t s, int j, uint32_t buf) __attribute__((always_inline)) {
+    const buffer from = buffer_of(x0, nb * a.cols * 2u);
+    each<NT * 4>([&](auto i) __attribute__((always_inline)) {
+      load16_lds(from, mine + buf * kBuf + i * kWideLoad, x[i], s * (kStepCols<kFp4> * 2u) + 64u * j);
+    });
   };
   const WeightLane<kFp4> lw(a.cols);
   WeightStep w[MT];
   // tiles past the last row repeat the first one and are not stored
-  auto codes = [&](uint32_t s, WeightStep* to) __attribute__((always_inline)) {
+  auto codes = [&](uint32_t s, auto tail, WeightStep* to) __attribute__((always_inline)) {
     each<MT>([&](auto m) __attribute__((always_inline)) {
       const uint64_t at = row0 + 16u * m;
       const WeightTile<kFp4> t(a.codes, a.scales, at < a.rows ? at : row0, a.rows, lw);
-      if (s < whole)
-        load_weights<kFp4, false>(lw, t, s, to[m]);
-      else
-        load_weights<kFp4, true>(lw, t, s, to[m]);
+      load_weights<kFp4, tail>(lw, t, s, to[m]);
     });
   };
   mfma_f32x4 acc[MT][NT];
   each<MT * NT>([&](auto i) __attribute__((always_inline)) { acc[i / NT][i % NT] = mfma_f32x4{0, 0, 0, 0}; });
-  if (s0 < s1) {
-    codes(s0, w);
-    stage(s0, std::integral_constant<int, 0>{}, 0);
-  }
-  for (uint32_t s = s0; s < s1; ++s) {
+  auto use = [&](auto j) __attribute__((always_inline)) {
+    const uint8_t* in = mine + (j % D) * kBuf + (r & 3u) * kWideLoad + (4u * (r >> 2) + 16u * h) * 16u;
+    each<4>([&](auto k) __attribute__((always_inline)) {
+      u32x4 xs[NT];
+      each<NT>([&](auto t) __attribute__((always_inline)) { xs[t] = *(const u32x4*)(in + t * 4u * kWideLoad + 16u * k); });
+      each<MT>([&](auto m) __attribute__((always_inline)) {
+        const u32x4 op = weight_operand<kFp4>(w[m], j, k);
+        each<NT>([&](auto t) __attribute__((always_inline)) { acc[m][t] = mfma16(op, xs[t], acc[m][t]); });
+      });
+    });
+  };
+  // A whole step, and (MORE) the loads of the one after it.
+  auto step = [&](uint32_t s, auto more) __attribute__((always_inline)) {
     each<MT>([&](auto m) __attribute__((always_inline)) { quad_transpose(w[m].v); });
     WeightStep next[MT];
     each<4>([&](auto j) __attribute__((always_inline)) {
-      wait_lgkm0();  // the other buffer has been read
-      wait_vm<0>();  // and this one is in
+      // Block j is in when only what was asked for after it is left: D - 2 more
+      // blocks, if there are as many, and the next step's codes if it was asked
+      // for before them.
+      constexpr int kAfter = more || D - 2 < 3 - j ? D - 2 : 3 - j;
+      wait_vm<kAfter * NT * 4 + (more && j >= 1 && j < D ? MT * kCodeLoads : 0)>();
+      wait_lgkm0();  // the buffer to fill has been read
       wave_lds_sync();
-      if constexpr (j < 3) {
-        stage(s, std::integral_constant<int, j + 1>{}, (j + 1u) & 1u);
-        if constexpr (j == 0) codes(s + 1u < s1 ? s + 1u : s, next);
-      } else if (s + 1u < s1) {
-        stage(s + 1u, std::integral_constant<int, 0>{}, 0);
+      constexpr int kTo = j + D - 1;
+      if constexpr (kTo < 4) stage(s, kTo, kTo % D);
+      if constexpr (kTo >= 4 && more) stage(s + 1u, kTo - 4, kTo % D);
+      load_fence();
+      if constexpr (j == 0 && more) {
+        codes(s + 1u, std::false_type{}, next);
+        load_fence();
       }
-      const uint8_t* in = mine + (j & 1u) * kBuf + (r & 3u) * kWideLoad + (4u * (r >> 2) + 16u * h) * 16u;
-      each<4>([&](auto k) __attribute__((always_inline)) {
-        u32x4 xs[NT];
-        each<NT>([&](auto t) __attribute__((always_inline)) { xs[t] = *(const u32x4*)(in + t * 4u * kWideLoad + 16u * k); });
-        each<MT>([&](auto m) __attribute__((always_inline)) {
-          const u32x4 op = weight_operand<kFp4>(w[m], j, k);
-          each<NT>([&](auto t) __attribute__((always_inline)) { acc[m][t] = mfma16(op, xs[t], acc[m][t]); });
-        });
-      });
+      use(j);
     });
-    each<MT>([&](auto m) __attribute__((always_inline)) { w[m] = next[m]; });
+    if constexpr (more) each<MT>([&](auto m) __attribute__((always_inline)) { w[m] = next[m]; });
+  };
+  const uint32_t end = s1 < whole ? s1 : whole;
+  if (s0 < end) {
+    codes(s0, std::false_type{}, w);
+    load_fence();
+    each<D - 1>([&](auto i) __attribute__((always_inline)) {
+      stage(s0, i, i);
+      load_fence();
+    });
+    for (uint32_t s = s0; s + 1u < end; ++s) step(s, std::true_type{});
+    step(end - 1u, std::false_type{});
+  }
+  if (s1 > whole && s0 < s1) {  // the short last step; cols is a multiple of 8: a piece is in or out
+    codes(whole, std::true_type{}, w);
+    each<MT>([&](auto m) __attribute__((always_inline)) { quad_transpose(w[m].v); });
+    each<4>([&](auto j) __attribute__((always_inline)) {
+      const uint32_t c = whole * kStepCols<kFp4> + 32u * j;
+      wait_lgkm0();
+      each<NT * 4>([&](auto i) __attribute__((always_inline)) {
+        *(u32x4*)(mine + (j % D) * kBuf + i * kWideLoad + 16u * lane) =
+            c + c0 < a.cols ? *(const u32x4*)((const uint8_t*)(x0 + c) + x[i]) : u32x4{0, 0, 0, 0};
+      });
+      wait_lgkm0();
+      wave_lds_sync();
+      use(j);
+    });
   }
   // the waves' sums, in order
   __syncthreads();
-  mfma_f32x4* const part = (mfma_f32x4*)lds;  // [KG][MT][NT][kWave]
+  mfma_f32x4* const part = (mfma_f32x4*)lds;  // [kWideWaves][MT][NT][kWave]
   each<MT * NT>([&](auto i) __attribute__((always_inline)) {
     part[(kg * MT * NT + i) * kWave + lane] = acc[i / NT][i % NT];
   });
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < MT * NT * kWave; i += kWave * KG) {
+  for (uint32_t i = threadIdx.x; i < MT * NT * kWave; i += kWave * kWideWaves) {
     mfma_f32x4 s = part[i];
 #pragma unroll
-    for (uint32_t v = 1; v < KG; ++v) s += part[v * (MT * NT * kWave) + i];
+    for (uint32_t v = 1; v < kWideWaves; ++v) s += part[v * (MT * NT * kWave) + i];
     const uint32_t l = i % kWave, t = i / kWave % NT, m = i / (kWave * NT);
     const uint32_t b = b0 + 16u * t + (l & 15u);
     const uint64_t y0 = row0 + 16u * m + 4u * (l >> 4);
@@ -296,41 +330,34 @@ void launch_rows(const Fp4Args& a, uint32_t row_blocks, uint32_t batch_blocks, h
     k_fp4_gemv<QUAD, true, 1><<<grid, kWave * waves, lds, s>>>(a);
 }
 
-template <int MT, int NT, int KG>
+template <int MT, int NT, int D>
 void launch_wide(const Fp4Args& a, hipStream_t s) {
   const uint32_t row_blocks = (uint32_t)((a.rows + MT * 16u - 1u) / (MT * 16u));
-  const size_t in = (size_t)KG * 2u * NT * 4u * kWideLoad, sums = (size_t)KG * MT * NT * 1024u;
-  k_fp4_wide<MT, NT, KG><<<dim3(row_blocks, (a.batch + 16u * NT - 1u) / (16u * NT)), kWave * KG,
+  const size_t in = (size_t)kWideWaves * D * NT * 4u * kWideLoad, sums = (size_t)kWideWaves * MT * NT * 1024u;
+  k_fp4_wide<MT, NT, D><<<dim3(row_blocks, (a.batch + 16u * NT - 1u) / (16u * NT)), kWave * kWideWaves,
                            in > sums ? in : sums, s>>>(a);
 }
 
-// At up to 16 input rows: blocks of 32 rows, two per compute unit (24576 x 6144,
-// batch 16: 27.0 -> 23.5 us; below that 16 rows and no LDS are faster: 4096 x 4096
-// 5.2 against 7.1).
-bool tall_enough(const Fp4Args& a) { return a.rows >= 32u * (cu_count() * 5u / 4u); }
+// Every block reads the inputs of its batch tiles whole, so the largest tile whose
+// blocks fill five eighths of the compute units is the fastest: 64 rows by 64 inputs
+// against 64 by 32 at 8192 x 8192: batch 128 30.6 us and 34.1, batch 64 (128 blocks
+// of the larger) 25.6 and 19.8; 64 by 32 against 32 by 32 at 14336 x 4096, batch 32:
+// 13.9 and 16.2, at 6144 x 24576 (96 of the larger) over 40 and 34.7; 32 by 32
+// against 32 by 16 at 4096 x 4096: batch 64 9.3 and 9.8, batch 32 (128) 7.8 and 6.5.
+uint32_t wide_blocks(const Fp4Args& a, uint32_t mt, uint32_t nt) {
+  return (uint32_t)((a.rows + 16u * mt - 1u) / (16u * mt)) * ((a.batch + 16u * nt - 1u) / (16u * nt));
+}
+uint32_t wide_enough() { return cu_count() * 5u / 8u; }
 
-// Every block reads the inputs of its batch tiles whole, so the tallest tile whose
-// blocks still fill the compute units is the fastest (6144 x 24576, batch 64: 64
-// rows 73.7 us, 32 rows 58.6; 14336 x 4096: 22.3, 28.4; 4096 x 4096 at two
-// tiles of inputs, 32 rows: 10.2 against 12.3 with four).  Blocks of four waves
-// where two or more of them go on a compute unit.
 void launch_wide_for(const Fp4Args& a, hipStream_t s) {
-  auto blocks = [&](uint32_t mt, uint32_t nt) {
-    return (a.rows + 16u * mt - 1u) / (16u * mt) * ((a.batch + 16u * nt - 1u) / (16u * nt));
-  };
-  const uint64_t enough = cu_count() * 5u / 8u;
-  if (a.batch <= 16)
-    launch_wide<2, 1, 4>(a, s);
-  else if (a.batch > 32 && blocks(4, 4) >= enough)
-    launch_wide<4, 4, 4>(a, s);
-  else if (a.batch > 32 && blocks(2, 4) >= enough)
-    launch_wide<2, 4, 4>(a, s);
-  else if (blocks(2, 2) >= 2u * enough)
-    launch_wide<2, 2, 4>(a, s);
-  else if (blocks(2, 2) >= enough)
-    launch_wide<2, 2, 8>(a, s);
+  if (a.batch > 32 && wide_blocks(a, 4, 4) >= wide_enough())
+    launch_wide<4, 4, 2>(a, s);
+  else if (a.batch > 16 && wide_blocks(a, 4, 2) >= wide_enough())
+    launch_wide<4, 2, 2>(a, s);
+  else if (a.batch > 16 && wide_blocks(a, 2, 2) >= wide_enough())
+    launch_wide<2, 2, 2>(a, s);
   else
-    launch_wide<1, 2, 8>(a, s);
+    launch_wide<2, 1, 4>(a, s);
 }
 
 uint32_t piece_blocks(uint64_t pieces) {
@@ -381,7 +408,7 @@ extern "C" int wc_fp4_gemv(const uint8_t* d_codes, const uint8_t* d_scales, uint
   const uint32_t rb = (uint32_t)row_blocks;
   if (batch <= 4)
     wc::launch_rows<true>(a, rb, 1, s);
-  else if (cols % 8u || (batch <= 16 && !wc::tall_enough(a)))
+  else if (cols % 8u || (batch <= 16 && wc::wide_blocks(a, 2, 1) < wc::wide_enough()))
     wc::launch_rows<false>(a, rb, (batch + 15u) / 16u, s);
   else
     wc::launch_wide_for(a, s);

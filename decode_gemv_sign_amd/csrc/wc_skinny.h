@@ -93,6 +93,12 @@ constexpr uint32_t kNowhere = 0xFFFFFF00u;
 __device__ __forceinline__ u32x4 load16(buffer b, uint32_t lane_off, uint32_t off) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)lane_off, (int)off, 0));
 }
+// 16 bytes per lane into LDS at dst + 16 * lane.  Buffer loads, as the compiler
+// waits for all loads where a register load was followed by one through a
+// pointer into LDS.
+__device__ __forceinline__ void load16_lds(buffer b, uint8_t* dst, uint32_t lane_off, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void_t*)dst, 16, (int)lane_off, (int)off, 0, 0);
+}
 
 // Values c .. c + 7 of a row of `cols` BF16 values (cols >= 1); what lies past
 // the row is 0.  Rows of an odd length start at any 2-byte address.  A piece that

@@ -165,13 +165,17 @@ __global__ __launch_bounds__(kWave * 16) void k_fp4_gemv(Fp4Args a) {
 }
 
 // Larger batches: MT x 16 weight rows by NT x 16 input rows per block, each of
-// its waves a run of the steps.  The inputs of one block of 128 columns
-// (wc_skinny.h) come to the wave's own part of LDS a block ahead, by global->LDS
-// loads: load i of a tile takes, lane 4b + k (+ 16 h), piece k of input row 4b + i,
-// so quads read 64 contiguous bytes, and the operand reads do the transposition;
-// 16 bytes of padding after every load put the pieces that one operand read takes
-// at a time in different banks.  Nothing is shared between waves until the end,
-// so there is no barrier for their loads to wait at.
+// its waves a run of the steps.  The inputs come to the wave's own part of LDS, by
+// buffer loads into LDS, D / 2 blocks of 128 columns (wc_skinny.h) at a time and as
+// many ahead: load i of a tile takes, lane 4b + k (+ 16 h), piece k of input row
+// 4b + i, so quads read 64 contiguous bytes, and the operand reads do the
+// transposition; 16 bytes of padding after every load put the pieces that one
+// operand read takes at a time in different banks.  Two blocks at a time are the
+// two halves of the cache lines of the inputs, which one at a time are mostly
+// fetched twice (8192 x 8192, batch 32: 14.2 us against 16.2); the larger tiles
+// take one, as LDS has to hold two such blocks per compute unit (24576 x 6144,
+// batch 64: 43.9 against 48.6).  Nothing is shared between waves until the end, so
+// there is no barrier for their loads to wait at.
 constexpr uint32_t kWideLoad = 1024u + 16u;
 constexpr uint32_t kWideWaves = 4;
 
@@ -184,6 +188,7 @@ __device__ __forceinline__ void load_fence() {
 template <int MT, int NT, int D>
 __global__ __launch_bounds__(kWave * kWideWaves) void k_fp4_wide(Fp4Args a) {
   constexpr uint32_t kBuf = NT * 4u * kWideLoad;
+  constexpr int P = D / 2;
   constexpr int kCodeLoads = 5;  // of a step of a tile: four of codes, one of scales
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // [kWideWaves][D][kBuf], then the sums
   const uint32_t lane = (uint32_t)lane_id(), kg = (uint32_t)wave_in_block();
@@ -203,10 +208,12 @@ __global__ __launch_bounds__(kWave * kWideWaves) void k_fp4_wide(Fp4Args a) {
     const uint32_t b = (i / 4u) * 16u + (r & ~3u) + i % 4u;
     x[i] = ((b < nb ? b : nb - 1u) * a.cols + c0) * 2u;
   });
-  auto stage = [&](uint32_t s, int j, uint32_t buf) __attribute__((always_inline)) {
+  // blocks j .. j + P - 1; the two halves of a cache line one after the other
+  auto stage = [&](uint32_t s, auto j) __attribute__((always_inline)) {
     const buffer from = buffer_of(x0, nb * a.cols * 2u);
-    each<NT * 4>([&](auto i) __attribute__((always_inline)) {
-      load16_lds(from, mine + buf * kBuf + i * kWideLoad, x[i], s * (kStepCols<kFp4> * 2u) + 64u * j);
+    each<NT * 4 * P>([&](auto i) __attribute__((always_inline)) {
+      load16_lds(from, mine + ((j + i % P) % D) * kBuf + (i / P) * kWideLoad, x[i / P],
+                 s * (kStepCols<kFp4> * 2u) + 64u * (j + i % P));
     });
   };
   const WeightLane<kFp4> lw(a.cols);
@@ -237,17 +244,17 @@ __global__ __launch_bounds__(kWave * kWideWaves) void k_fp4_wide(Fp4Args a) {
     each<MT>([&](auto m) __attribute__((always_inline)) { quad_transpose(w[m].v); });
     WeightStep next[MT];
     each<4>([&](auto j) __attribute__((always_inline)) {
-      // Block j is in when only what was asked for after it is left: D - 2 more
-      // blocks, if there are as many, and the next step's codes if it was asked
-      // for before them.
-      constexpr int kAfter = more || D - 2 < 3 - j ? D - 2 : 3 - j;
-      wait_vm<kAfter * NT * 4 + (more && j >= 1 && j < D ? MT * kCodeLoads : 0)>();
-      wait_lgkm0();  // the buffer to fill has been read
-      wave_lds_sync();
-      constexpr int kTo = j + D - 1;
-      if constexpr (kTo < 4) stage(s, kTo, kTo % D);
-      if constexpr (kTo >= 4 && more) stage(s + 1u, kTo - 4, kTo % D);
-      load_fence();
+      if constexpr (j % P == 0) {
+        // blocks j .. j + P - 1 are in when no load is left but those of the next
+        // step's codes, which at j == P were asked for after them
+        wait_vm<(more && j == P ? MT * kCodeLoads : 0)>();
+        wait_lgkm0();  // the buffers to fill have been read
+        wave_lds_sync();
+        constexpr int kTo = j + P;
+        if constexpr (kTo < 4) stage(s, std::integral_constant<int, kTo>{});
+        if constexpr (kTo >= 4 && more) stage(s + 1u, std::integral_constant<int, kTo - 4>{});
+        load_fence();
+      }
       if constexpr (j == 0 && more) {
         codes(s + 1u, std::false_type{}, next);
         load_fence();
@@ -260,10 +267,8 @@ __global__ __launch_bounds__(kWave * kWideWaves) void k_fp4_wide(Fp4Args a) {
   if (s0 < end) {
     codes(s0, std::false_type{}, w);
     load_fence();
-    each<D - 1>([&](auto i) __attribute__((always_inline)) {
-      stage(s0, i, i);
-      load_fence();
-    });
+    stage(s0, std::integral_constant<int, 0>{});
+    load_fence();
     for (uint32_t s = s0; s + 1u < end; ++s) step(s, std::true_type{});
     step(end - 1u, std::false_type{});
   }
@@ -342,8 +347,8 @@ void launch_wide(const Fp4Args& a, hipStream_t s) {
 // blocks fill five eighths of the compute units is the fastest: 64 rows by 64 inputs
 // against 64 by 32 at 8192 x 8192: batch 128 30.6 us and 34.1, batch 64 (128 blocks
 // of the larger) 25.6 and 19.8; 64 by 32 against 32 by 32 at 14336 x 4096, batch 32:
-// 13.9 and 16.2, at 6144 x 24576 (96 of the larger) over 40 and 34.7; 32 by 32
-// against 32 by 16 at 4096 x 4096: batch 64 9.3 and 9.8, batch 32 (128) 7.8 and 6.5.
+// 13.9 and 16.2, at 8192 x 8192 (128 of the larger) 18.0 and 14.2; 32 by 32
+// against 32 by 16 at 4096 x 4096: batch 64 8.3 and 8.9, batch 32 (128) 7.5 and 6.3.
 uint32_t wide_blocks(const Fp4Args& a, uint32_t mt, uint32_t nt) {
   return (uint32_t)((a.rows + 16u * mt - 1u) / (16u * mt)) * ((a.batch + 16u * nt - 1u) / (16u * nt));
 }
@@ -355,7 +360,7 @@ void launch_wide_for(const Fp4Args& a, hipStream_t s) {
   else if (a.batch > 16 && wide_blocks(a, 4, 2) >= wide_enough())
     launch_wide<4, 2, 2>(a, s);
   else if (a.batch > 16 && wide_blocks(a, 2, 2) >= wide_enough())
-    launch_wide<2, 2, 2>(a, s);
+    launch_wide<2, 2, 4>(a, s);
   else
     launch_wide<2, 1, 4>(a, s);
 }

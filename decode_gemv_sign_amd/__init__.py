@@ -511,11 +511,12 @@ def fp4_encode(w: torch.Tensor, out: Fp4 | None = None, stream=None) -> Fp4:
         out = Fp4(torch.empty((*w.shape[:-1], 16 * groups), dtype=torch.uint8, device=w.device),
                   torch.empty((*w.shape[:-1], groups), dtype=torch.uint8, device=w.device), cols)
         _used_on(stream, out.codes, out.scales)
-    _fp4(out, "out")
-    if tuple(out.scales.shape) != (*w.shape[:-1], groups) or out.cols != cols:
-        raise ValueError(f"out holds {tuple(out.scales.shape[:-1])} rows of {out.cols} columns, "
-                         f"w has shape {tuple(w.shape)}")
-    _same_device("fp4_encode", w, out.codes, out.scales)
+    else:
+        _fp4(out, "out")
+        if tuple(out.scales.shape) != (*w.shape[:-1], groups) or out.cols != cols:
+            raise ValueError(f"out holds {tuple(out.scales.shape[:-1])} rows of {out.cols} columns, "
+                             f"w has shape {tuple(w.shape)}")
+        _same_device("fp4_encode", w, out.codes, out.scales)
     _check(_lib.wc_fp4_encode(_ptr(w), w.shape[:-1].numel(), cols, _ptr(out.codes),
                               _ptr(out.scales), _stream(stream)), "wc_fp4_encode")
     return out
@@ -528,8 +529,7 @@ def fp4_decode(q: Fp4, out: torch.Tensor | None = None, stream=None) -> torch.Te
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=q.codes.device)
         _used_on(stream, out)
-    out = _bits16(out, "out")
-    if tuple(out.shape) != shape:
+    elif tuple(_bits16(out, "out").shape) != shape:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
     _same_device("fp4_decode", q.codes, q.scales, out)
     _check(_lib.wc_fp4_decode(_ptr(q.codes), _ptr(q.scales), out.shape[:-1].numel(), cols,

@@ -45,7 +45,10 @@ __device__ inline uint32_t max_abs8(u32x4 w) {
 }
 
 // A lane codes 8 columns; the four lanes of a group share their maximum.
-// Blocks walk the rows' pieces of 8 columns, `pieces` = 4 G per row.
+// Blocks walk the rows' pieces of 8 columns, 4 G per row.  Bound by HBM:
+// 24576 x 6144 in 96 us, 382 MB at 4.0 TB/s (a plain copy of 2 GiB: 4.9); four
+// pieces' loads in flight per lane instead of one took 107.  1000 x 4100: 4.4 us,
+// of which 2.4 are an empty kernel's.
 __global__ __launch_bounds__(kBlockThreads) void k_fp4_encode(const uint16_t* __restrict__ w,
                                                               uint64_t rows, uint32_t cols,
                                                               uint32_t groups,
@@ -70,6 +73,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_fp4_encode(const uint16_t* __
   }
 }
 
+// A lane rebuilds 8 columns.  Bound by HBM: 24576 x 6144 in 65 us, 382 MB at 5.9 TB/s.
 __global__ __launch_bounds__(kBlockThreads) void k_fp4_decode(const uint8_t* __restrict__ codes,
                                                               const uint8_t* __restrict__ scales,
                                                               uint64_t rows, uint32_t cols,
@@ -101,10 +105,21 @@ struct Fp4Args {
   uint32_t cols, batch;
 };
 
-// 16 rows per block, up to 16 input rows (QUAD: up to 4).  Each wave takes a run
+// y = W x, the codes rebuilt as BF16 operands (exact: a magnitude has two bits)
+// and summed in fp32 by the matrix cores.  16 rows per block, up to 16 input rows
+// (QUAD: up to 4, each input loaded once, with no transposition; Sums in
+// wc_skinny.h).  Each wave takes a run
 // of the steps, and their sums are added in LDS in wave order.  Input rows past
-// the batch repeat the last one and are not stored.
-template <bool QUAD, bool ANY, int U>
+// the batch repeat the last one and are not stored.  ANY: rows of inputs that do
+// not start at 16-byte boundaries.
+// At one to four inputs it is bound by HBM: 24576 x 6144, batch 1: 80 MB in 16.5 us,
+// 4.9 TB/s (6.2 is the most a read-only kernel reached from HBM); 14336 x 4096,
+// batch 4: 32 MB in 8.5 us, of which 2.4 are an empty kernel's.  A small call is
+// launch and one trip to memory: 1024 x 4096 in 3.7 us.  At 5 to 16 the inputs'
+// loads and their transposition count as much as the codes: 5003 x 4100, batch 16:
+// 10.2 us.  Loading several steps at once, or as a pipeline, took longer at every
+// size: the loads are bound by their address cycles, not by their latency.
+template <bool QUAD, bool ANY>
 __global__ __launch_bounds__(kWave * 16) void k_fp4_gemv(Fp4Args a) {
   extern __shared__ mfma_f32x4 part[];  // [waves][kWave]
   const uint32_t lane = (uint32_t)lane_id(), wave = (uint32_t)wave_in_block();
@@ -134,7 +149,7 @@ __global__ __launch_bounds__(kWave * 16) void k_fp4_gemv(Fp4Args a) {
   const uint32_t whole = a.cols / kStepCols<kFp4>;
   const uint32_t steps = (a.cols + kStepCols<kFp4> - 1u) / kStepCols<kFp4>;
   const uint32_t s0 = wave * steps / waves, s1 = (wave + 1u) * steps / waves;
-  step_batches<U, Slot>(
+  step_batches<1, Slot>(
       (s1 < whole ? s1 : whole) - s0,
       [&](uint32_t q, Slot& s) __attribute__((always_inline)) {
         load_weights<kFp4, false>(lw, w, s0 + q, s.w);
@@ -176,6 +191,10 @@ __global__ __launch_bounds__(kWave * 16) void k_fp4_gemv(Fp4Args a) {
 // take one, as LDS has to hold two such blocks per compute unit (24576 x 6144,
 // batch 64: 43.9 against 48.6).  Nothing is shared between waves until the end, so
 // there is no barrier for their loads to wait at.
+// 6144 x 24576, batch 32: 83 MB in 28.6 to 32 us; without the inputs' loads it took
+// 22, without the codes' 31, without the products as long: it waits for the inputs,
+// 1.5 MB from L2 per compute unit.  4096 x 4096, batch 256: 17.5 us, 490 TFLOP/s, of
+// which the blocks' first loads and the launch are about 5.
 constexpr uint32_t kWideLoad = 1024u + 16u;
 constexpr uint32_t kWideWaves = 4;
 
@@ -330,9 +349,9 @@ void launch_rows(const Fp4Args& a, uint32_t row_blocks, uint32_t batch_blocks, h
   const dim3 grid(row_blocks, batch_blocks);
   const size_t lds = waves * kWave * sizeof(mfma_f32x4);
   if (a.cols % 8u == 0)
-    k_fp4_gemv<QUAD, false, 1><<<grid, kWave * waves, lds, s>>>(a);
+    k_fp4_gemv<QUAD, false><<<grid, kWave * waves, lds, s>>>(a);
   else
-    k_fp4_gemv<QUAD, true, 1><<<grid, kWave * waves, lds, s>>>(a);
+    k_fp4_gemv<QUAD, true><<<grid, kWave * waves, lds, s>>>(a);
 }
 
 template <int MT, int NT, int D>

@@ -239,9 +239,9 @@ __device__ __forceinline__ u32x4 weight_operand(const WeightStep& s, int j, int 
 
 // n steps, U at a time: the loads of U steps go out together, then the steps are
 // used; the other waves of the compute unit have theirs in flight meanwhile.
-// Loading a step ahead of its use measured slower here: past the end such a
-// pipeline either loads for nothing (each load costs its address cycles) or
-// branches, and then every wait is for all loads.
+// Loading a step ahead of its use measured slower where a wave has few steps: past
+// the end such a pipeline either loads for nothing (each load costs its address
+// cycles) or branches, and then every wait is for all loads.
 template <int U, typename Slot, typename Load, typename Use>
 __device__ __forceinline__ void step_batch(uint32_t q, Load&& load, Use&& use) {
   Slot s[U];

@@ -17,8 +17,9 @@
  *                 down[e] (silu(gate[e] x[t]) * (up[e] x[t]))
  * silu(a) = a / (1 + exp(-a)).  A token with no expert at all gets y = 0.
  *
- * Sums and scores are fp32; weight * silu(gate) * up is rounded to BF16 once,
- * as the operand of the second product, and y once at the end.  The sums'
+ * Sums and scores are fp32; weight * silu(gate) * up goes into the second
+ * product as the sum of two BF16 numbers (16 bits of it), and y is rounded to
+ * BF16 once at the end.  The sums'
  * order is fixed by the shape: the same call gives the same bits.
  *
  * Conventions as in wc.h.  d_x, d_router, the weights' d_data and d_work are

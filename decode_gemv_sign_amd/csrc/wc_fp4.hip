@@ -46,9 +46,10 @@ __device__ inline uint32_t max_abs8(u32x4 w) {
 
 // A lane codes 8 columns; the four lanes of a group share their maximum.
 // Blocks walk the rows' pieces of 8 columns, 4 G per row.  Bound by HBM:
-// 24576 x 6144 in 96 us, 382 MB at 4.0 TB/s (a plain copy of 2 GiB: 4.9); four
-// pieces' loads in flight per lane instead of one took 107.  1000 x 4100: 4.4 us,
-// of which 2.4 are an empty kernel's.
+// 24576 x 6144 in 69 us, 382 MB at 5.5 TB/s (a plain copy of 2 GiB: 4.9); 96 us with
+// loads that leave the weights, which nothing reads again, in the caches, and 107
+// with four of those in flight per lane.  1000 x 4100: 4.4 us, of which 2.4 are an
+// empty kernel's.
 __global__ __launch_bounds__(kBlockThreads) void k_fp4_encode(const uint16_t* __restrict__ w,
                                                               uint64_t rows, uint32_t cols,
                                                               uint32_t groups,
@@ -61,7 +62,8 @@ __global__ __launch_bounds__(kBlockThreads) void k_fp4_encode(const uint16_t* __
     const uint64_t row = p / (groups * 4u);
     const uint32_t c = (uint32_t)(p - row * (groups * 4u)) * 8u;
     const uint16_t* from = w + row * cols;
-    const u32x4 v = c + 8u <= cols ? *(const u32x4_any*)(from + c) : load8(from, c, cols);
+    const u32x4 v =
+        c + 8u <= cols ? (u32x4)__builtin_nontemporal_load((const u32x4_any*)(from + c)) : load8(from, c, cols);
     uint32_t m = max_abs8(v);
     const uint32_t a = (uint32_t)__shfl_xor((int)m, 1, kWave);
     m = m > a ? m : a;
@@ -73,7 +75,8 @@ __global__ __launch_bounds__(kBlockThreads) void k_fp4_encode(const uint16_t* __
   }
 }
 
-// A lane rebuilds 8 columns.  Bound by HBM: 24576 x 6144 in 65 us, 382 MB at 5.9 TB/s.
+// A lane rebuilds 8 columns.  Bound by HBM: 24576 x 6144 in 57 us, 387 MB
+// at 6.8 TB/s (65 with stores that stay in the caches).
 __global__ __launch_bounds__(kBlockThreads) void k_fp4_decode(const uint8_t* __restrict__ codes,
                                                               const uint8_t* __restrict__ scales,
                                                               uint64_t rows, uint32_t cols,
@@ -87,7 +90,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_fp4_decode(const uint8_t* __r
     const u32x4 v = fp4_expand(((const uint32_t*)codes)[p], fp4_scale(scales[p / 4u]));
     uint16_t* o = out + row * cols + c;
     if (c + 8u <= cols) {
-      *(u32x4_any*)o = v;
+      __builtin_nontemporal_store((u32x4_any)v, (u32x4_any*)o);
     } else {
 #pragma unroll
       for (uint32_t i = 0; i < 7; ++i)

@@ -35,7 +35,8 @@ struct MoeUnit {
   uint16_t expert;
   uint16_t place;  // of its first token among the chosen pairs
   uint16_t count;  // its tokens
-  uint16_t pair;   // k_moe_down: 1 and 2 for two units that go together, else 0
+  uint16_t pair;   // k_moe_gate_up: 0 for an expert's only unit, else 1; k_moe_down:
+                   // 1 and 2 for two units that go together, else 0
 };
 
 // The choice, as k_moe_down needs it.
@@ -337,13 +338,14 @@ __device__ inline void choose(const MoeArgs& a, uint32_t t, MoeChoice& c) {
   }
 }
 
-// Units of up to `size` of an expert's tokens, at `at` and after; `pairs`: in pairs.
+// Units of up to `size` of an expert's tokens, at `at` and after; `pairs`: for
+// k_moe_down.
 __device__ inline void fill_units(MoeUnit* unit, uint32_t at, uint32_t e, uint32_t first, uint32_t n,
                                   uint32_t size, bool pairs) {
   for (uint32_t m = 0; m < n; m += size) {
     const bool second = m / size & 1u, one = !second && m + size >= n;
     unit[at++] = MoeUnit{(uint16_t)e, (uint16_t)(first + m), (uint16_t)(n - m < size ? n - m : size),
-                         (uint16_t)(!pairs || one ? 0 : second ? 2 : 1)};
+                         (uint16_t)(!pairs ? n > size : one ? 0 : second ? 2 : 1)};
   }
 }
 
@@ -409,11 +411,14 @@ __device__ inline void choose_all(const MoeArgs& a, MoeChoice& c, MoeRoute* rout
 // of steps, and a tile that several waves worked on is joined in LDS, in wave
 // order.  A wave loads one step ahead: its runs are long, and past the end it does
 // not load.
+// The weights of experts with one unit of tokens pass the caches by; those of more
+// units do not, as the next tile reads them again (64 tokens, 8 experts of 2048 x 4096,
+// 2 each: 122 us for the layer, 129 if they do).
 // Bound by HBM where there are many weights: BF16, 32 experts of 2048 x 4096, 2
-// tokens, 4 each: 252 MB in 49 us, 5.1 TB/s; 64 experts of 1024 x 2048, 64 tokens: 537
-// MB in 110 us, 4.9 TB/s; 4-bit, 128 experts of 1024 x 4096, 16 tokens: 365 MB in 80 us,
-// 4.6 TB/s.  One token of 64 experts of 1408 x 2048, 4-bit: 18 MB in 13.5 us, most
-// of it the launch, the choice and the inputs before the first product.
+// tokens, 4 each: 252 MB in 46 us, 5.5 TB/s; 64 experts of 1024 x 2048, 64 tokens: 537
+// MB in 100 us, 5.4 TB/s; 4-bit, 128 experts of 1024 x 4096, 16 tokens: 365 MB in 71 us,
+// 5.1 TB/s.  One token of 64 experts of 1408 x 2048, 4-bit: 18 MB in 14 us, most of it
+// the launch, the choice and the inputs before the first product.
 template <int KIND>
 __global__ __launch_bounds__(kWave * kUpWaves, 3) void k_moe_gate_up(MoeArgs a) {
   __shared__ MoeChoice c;
@@ -492,12 +497,15 @@ __global__ __launch_bounds__(kWave * kUpWaves, 3) void k_moe_gate_up(MoeArgs a) 
       const uint64_t row = e * 2u * a.inter + lt * kRowTile;
       const WeightTile<KIND> wg(a.gu, a.gu_scales, row, rows, lw);
       const WeightTile<KIND> wu(a.gu, a.gu_scales, row + a.inter, rows, lw);
-      if (ls < whole) {
-        load_weights<KIND, false>(lw, wg, ls, s.g);
-        load_weights<KIND, false>(lw, wu, ls, s.u);
-      } else {
+      if (ls >= whole) {
         load_weights<KIND, true>(lw, wg, ls, s.g);
         load_weights<KIND, true>(lw, wu, ls, s.u);
+      } else if (c.unit[lu].pair == 0) {
+        load_weights<KIND, false, true>(lw, wg, ls, s.g);
+        load_weights<KIND, false, true>(lw, wu, ls, s.u);
+      } else {
+        load_weights<KIND, false>(lw, wg, ls, s.g);
+        load_weights<KIND, false>(lw, wu, ls, s.u);
       }
       advance(lu, lt, ls);
     };
@@ -594,12 +602,12 @@ __global__ __launch_bounds__(kWave * kUpWaves, 3) void k_moe_gate_up(MoeArgs a) 
 // order, a run of them per part, and of that per wave; an expert's units go two by
 // two, taking turns at the same columns, so that its weights come from memory once
 // for 16 tokens (64 tokens, 8 of 64 experts each: 60 us and 1.08 times the weights'
-// bytes, against 63 and 1.44).  Lane column n takes the high part of token
+// bytes, against 63 and 1.44); units without a second one pass the caches by (58).  Lane column n takes the high part of token
 // n & 7 of the unit, or (n >= 8) the low part.  When a unit is done, its sums go to
 // the wave's own [token][16] array in LDS; at the end these are added over the
 // waves, and over the parts by the last block to arrive, in order both.
-// BF16, 2 tokens as above: 126 MB in 22.4 us, 5.6 TB/s; 4-bit, 16 tokens: 182 MB in 42 to
-// 47 us, 4.1 TB/s; one token: 9 MB in 6.4 us.  12 waves took the same as 16; the
+// BF16, 2 tokens as above: 126 MB in 21.4 us, 5.9 TB/s; 4-bit, 16 tokens: 182 MB in 39 to
+// 47 us; one token: 9 MB in 7 us.  12 waves took the same as 16; the
 // operands of the activations loaded by quads and transposed here instead of stored
 // in operand order by k_moe_gate_up spilled registers and took longer.
 template <int KIND, int U>
@@ -660,10 +668,12 @@ __global__ __launch_bounds__(kWave * kDownWaves) void k_moe_down(MoeArgs a) {
         const MoeUnit un = unit[lu];
         const uint64_t e = (uint32_t)__builtin_amdgcn_readfirstlane((int)un.expert);
         const WeightTile<KIND> w(a.dn, a.dn_scales, e * a.hidden + row0, (uint64_t)a.experts * a.hidden, lw);
-        if (ls < whole)
-          load_weights<KIND, false>(lw, w, ls, s.w);
-        else
+        if (ls >= whole)
           load_weights<KIND, true>(lw, w, ls, s.w);
+        else if (un.pair == 0)
+          load_weights<KIND, false, true>(lw, w, ls, s.w);
+        else
+          load_weights<KIND, false>(lw, w, ls, s.w);
         const uint32_t i = r & 7u, last = un.count - 1u;  // columns past the tokens repeat the last one
         const u32x4* x = act_of(a, un) + 2u * (i < last ? i : last) + (r >> 3);
         each<4 * kB>([&](auto q) __attribute__((always_inline)) {

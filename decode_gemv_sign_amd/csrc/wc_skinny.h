@@ -90,8 +90,9 @@ __device__ __forceinline__ buffer buffer_of(const void* p, uint32_t n) {
   return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)n, 0x00027000);
 }
 constexpr uint32_t kNowhere = 0xFFFFFF00u;
+template <bool ONCE = false>  // ONCE: what nothing reads again; the caches let it go first
 __device__ __forceinline__ u32x4 load16(buffer b, uint32_t lane_off, uint32_t off) {
-  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)lane_off, (int)off, 0));
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)lane_off, (int)off, ONCE ? 2 : 0));
 }
 // 16 bytes per lane into LDS at dst + 16 * lane.  Buffer loads, as the compiler
 // waits for all loads where a register load was followed by one through a
@@ -192,7 +193,11 @@ struct WeightStep {
 };
 
 // TAIL: the row's last step, of which some columns do not exist: they read as 0.
-template <int KIND, bool TAIL>
+// ONCE: for weights that no other tile of inputs needs.  It pays in the MoE
+// kernels, where an expert's matrices are one tile's (128 experts, 16 tokens, 4-bit:
+// 139 -> 124 us; 32 experts, BF16, 2 tokens: 80 -> 73.5); the 4-bit GEMV took longer with it
+// (24576 x 6144, batch 1: 16.4 -> 18.2).
+template <int KIND, bool TAIL, bool ONCE = false>
 __device__ __forceinline__ void load_weights(const WeightLane<KIND>& l, const WeightTile<KIND>& w,
                                              uint32_t step, WeightStep& s) {
   const uint32_t lane = (uint32_t)lane_id(), r = lane & 15u, h = lane >> 4, j = lane & 3u;
@@ -200,7 +205,7 @@ __device__ __forceinline__ void load_weights(const WeightLane<KIND>& l, const We
     const buffer b = buffer_of(w.data, w.n * l.row_bytes);  // rows past the end read as 0
     const bool in = !TAIL || step * 16u + 4u * h + j < l.groups;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s.v[i] = load16(b, in ? l.off[i] : kNowhere, step * 256u);
+    for (int i = 0; i < 4; ++i) s.v[i] = load16<ONCE>(b, in ? l.off[i] : kNowhere, step * 256u);
     const uint8_t* scales = w.scales + (r < w.n ? l.scale_off : 4u * h) + step * 16u;
     if constexpr (TAIL) {
       s.e = 0;
@@ -214,7 +219,7 @@ __device__ __forceinline__ void load_weights(const WeightLane<KIND>& l, const We
     const buffer b = buffer_of(w.data, w.n * l.row_bytes);
     const bool in = !TAIL || step * 128u + 32u * h + 8u * j < l.cols;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s.v[i] = load16(b, in ? l.off[i] : kNowhere, step * 256u);
+    for (int i = 0; i < 4; ++i) s.v[i] = load16<ONCE>(b, in ? l.off[i] : kNowhere, step * 256u);
   } else {
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i) {

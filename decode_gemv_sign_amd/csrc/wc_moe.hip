@@ -454,9 +454,11 @@ __global__ __launch_bounds__(kWave * kUpWaves, 3) void k_moe_gate_up(MoeArgs a) 
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      // weight * silu(gate) * up, as the sum of two BF16 (16 bits of it)
+      // weight * silu(gate) * up, as the sum of two BF16 (16 bits of it).  A finite v that
+      // rounds past BF16's range keeps its largest number and leaves the rest to the low part.
       const float v = i0 + k < a.inter ? g[k] / (1.0f + expf(-g[k])) * u[k] * weight : 0.0f;
       hi[k] = bf16_of(v);
+      if ((hi[k] & 0x7FFFu) == 0x7F80u && fabsf(v) < INFINITY) --hi[k];
       const float rest = v - __uint_as_float(hi[k] << 16);
       lo[k] = rest == rest ? bf16_of(rest) : 0u;  // v infinite or NaN: the high part says so
     }

@@ -636,10 +636,14 @@ __global__ __launch_bounds__(kWave * kDownWaves) void k_moe_down(MoeArgs a) {
   auto flush = [&](mfma_f32x4& acc, uint32_t which) __attribute__((always_inline)) {
     if (which == 0xFFFFFFFFu) return;
     const MoeUnit un = unit[which];
+    // lane r < 8 adds the sum of its token's low parts (lane r + 8) to that of the high parts.
+    // Where the latter is infinite or NaN it is the result: an infinite weight times a
+    // low part of 0 or of the other sign would make it NaN.
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float s = acc[k];
-      acc[k] = s + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(s), 0x128, 0xF, 0xF, false));
+      const float low = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(s), 0x128, 0xF, 0xF, false));
+      acc[k] = fabsf(s) < INFINITY ? s + low : s;
     }
     if (r < un.count) {
       mfma_f32x4* o = (mfma_f32x4*)(mine + token[un.place + r] * 16u) + h;

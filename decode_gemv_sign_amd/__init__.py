@@ -493,11 +493,21 @@ def _fp4(q: Fp4, what: str):
 
 
 def _used_on(stream, *tensors):
-    """Memory allocated here on the current stream and used on another one is
-    not handed out again before that one is done with it."""
+    """Memory of another stream's pool that the caller reads on the current
+    stream is not handed out again before that one is done with it."""
     if stream is not None and stream.cuda_stream != _stream():
         for t in tensors:
-            t.record_stream(stream)
+            t.record_stream(torch.cuda.current_stream())
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory for a call on `stream` (None: the current one) to write.  It is
+    taken from that stream's pool: what was freed to the current stream's may
+    still be in use by work queued there, which `stream` does not wait for."""
+    if stream is None or stream.cuda_stream == _stream():
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def fp4_encode(w: torch.Tensor, out: Fp4 | None = None, stream=None) -> Fp4:
@@ -508,8 +518,8 @@ def fp4_encode(w: torch.Tensor, out: Fp4 | None = None, stream=None) -> Fp4:
     cols = w.shape[-1]
     groups = (cols + FP4_GROUP - 1) // FP4_GROUP
     if out is None:
-        out = Fp4(torch.empty((*w.shape[:-1], 16 * groups), dtype=torch.uint8, device=w.device),
-                  torch.empty((*w.shape[:-1], groups), dtype=torch.uint8, device=w.device), cols)
+        out = Fp4(_empty((*w.shape[:-1], 16 * groups), torch.uint8, w.device, stream),
+                  _empty((*w.shape[:-1], groups), torch.uint8, w.device, stream), cols)
         _used_on(stream, out.codes, out.scales)
     else:
         _fp4(out, "out")
@@ -527,7 +537,7 @@ def fp4_decode(q: Fp4, out: torch.Tensor | None = None, stream=None) -> torch.Te
     lead, rows, cols = _fp4(q, "q")
     shape = (*lead, rows, cols)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.codes.device)
+        out = _empty(shape, torch.bfloat16, q.codes.device, stream)
         _used_on(stream, out)
     elif tuple(_bits16(out, "out").shape) != shape:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
@@ -545,7 +555,7 @@ def fp4_gemv(q: Fp4, x: torch.Tensor, out: torch.Tensor | None = None, stream=No
     x = _bits16(x, "x")
     batch = _batch_of(x, cols)
     if out is None:
-        out = torch.empty((batch, rows), dtype=torch.float32, device=x.device)
+        out = _empty((batch, rows), torch.float32, x.device, stream)
         _used_on(stream, out)
     _gemv_out(out, batch, rows)
     _same_device("fp4_gemv", q.codes, q.scales, x, out)
@@ -622,16 +632,15 @@ def moe(x: torch.Tensor, router: torch.Tensor, gate_up, down, top_k: int, *, sco
             raise ValueError(f"bias must be a contiguous [{experts}], got {tuple(bias.shape)}")
     need = moe_workspace_bytes(tokens, hidden, inter, experts, top_k)
     if work is None:
-        work = torch.empty(need, dtype=torch.uint8, device=x.device)
-        _used_on(stream, work)
+        work = _empty(need, torch.uint8, x.device, stream)
     _bytes(work, "work", need)
     if out is None:
-        out = torch.empty((tokens, hidden), dtype=torch.bfloat16, device=x.device)
+        out = _empty((tokens, hidden), torch.bfloat16, x.device, stream)
         _used_on(stream, out)
     if tuple(_bits16(out, "out").shape) != (tokens, hidden):
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(tokens, hidden)}")
-    ids = torch.empty((tokens, top_k), dtype=torch.int32, device=x.device)
-    weights = torch.empty((tokens, top_k), dtype=torch.float32, device=x.device)
+    ids = _empty((tokens, top_k), torch.int32, x.device, stream)
+    weights = _empty((tokens, top_k), torch.float32, x.device, stream)
     _used_on(stream, ids, weights)
     _same_device("moe", x, router, work, out, *tgu, *tdn, *(() if bias is None else (bias,)))
     shape = _moe_shape(tokens, hidden, inter, experts, top_k, scoring, renorm, scale)

@@ -166,6 +166,24 @@ def _stream(stream=None) -> int:
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _used_on(stream, *tensors):
+    """Memory of another stream's pool that the caller reads on the current
+    stream is not handed out again before that one is done with it."""
+    if stream is not None and stream.cuda_stream != _stream():
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream())
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory for a call on `stream` (None: the current one) to write.  It is
+    taken from that stream's pool: what was freed to the current stream's may
+    still be in use by work queued there, which `stream` does not wait for."""
+    if stream is None or stream.cuda_stream == _stream():
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _on_device(t: torch.Tensor) -> bool:
     """True for a tensor in GPU memory (the library takes device pointers only)."""
     return t.is_cuda
@@ -242,8 +260,8 @@ def workspace_bytes(n: int) -> int:
     return 20528 + (16 + 6 * STAGE_SYMBOLS) * ((n + 8191) // 8192)
 
 
-def _workspace(n: int, device) -> torch.Tensor:
-    return torch.empty(workspace_bytes(n), dtype=torch.uint8, device=device)
+def _workspace(n: int, device, stream) -> torch.Tensor:
+    return _empty(workspace_bytes(n), torch.uint8, device, stream)
 
 
 def build_dict(w: torch.Tensor, layout: int, work: torch.Tensor | None = None,
@@ -252,7 +270,7 @@ def build_dict(w: torch.Tensor, layout: int, work: torch.Tensor | None = None,
     w = _bits16(w, "w")
     n = w.numel()
     if work is None:
-        work = _workspace(n, w.device)
+        work = _workspace(n, w.device, stream)
     _bytes(work, "work", workspace_bytes(n))
     _same_device("build_dict", w, work)
     h = Header()
@@ -269,7 +287,7 @@ def encode_into(h: Header, w: torch.Tensor, container: torch.Tensor,
         raise ValueError(f"w has {w.numel()} weights, the header {h.n}")
     _bytes(container, "container", h.total_bytes)
     if work is None:
-        work = _workspace(w.numel(), w.device)
+        work = _workspace(w.numel(), w.device, stream)
     _bytes(work, "work", workspace_bytes(w.numel()))
     _same_device("encode_into", w, container, work)
     _check(_lib.wc_encode(ctypes.byref(h), _ptr(w), _ptr(container), container.numel(),
@@ -295,9 +313,10 @@ def encode_into_noalloc(h: Header, w: torch.Tensor, container: torch.Tensor,
 def encode(w: torch.Tensor, layout: int, stream=None):
     """(header, container): dictionary, then the whole container on the device."""
     w = _bits16(w, "w")
-    work = _workspace(w.numel(), w.device)
+    work = _workspace(w.numel(), w.device, stream)
     h = build_dict(w, layout, work, stream)
-    c = torch.empty(h.total_bytes, dtype=torch.uint8, device=w.device)
+    c = _empty(h.total_bytes, torch.uint8, w.device, stream)
+    _used_on(stream, c)
     encode_into(h, w, c, work, stream)
     return h, c
 
@@ -312,7 +331,8 @@ def decode(h: Header, container: torch.Tensor, out: torch.Tensor | None = None,
     """wc_decode: the n BF16 bit patterns (int16 tensor unless `out` is given)."""
     _bytes(container, "container", h.total_bytes)
     if out is None:
-        out = torch.empty(h.n, dtype=torch.int16, device=container.device)
+        out = _empty(h.n, torch.int16, container.device, stream)
+        _used_on(stream, out)
     out = _bits16(out, "out")
     if out.numel() < h.n:
         raise ValueError(f"out holds {out.numel()} weights, {h.n} needed")
@@ -331,7 +351,8 @@ def decode_gemv(h: Header, container: torch.Tensor, rows: int, cols: int, x: tor
     x = _bits16(x, "x")
     batch = _batch_of(x, cols)
     if out is None:
-        out = torch.empty((batch, rows), dtype=torch.float32, device=container.device)
+        out = _empty((batch, rows), torch.float32, container.device, stream)
+        _used_on(stream, out)
     _gemv_out(out, batch, rows)
     _same_device("decode_gemv", container, x, out)
     _check(_lib.wc_decode_gemv(ctypes.byref(h), _ptr(container), container.numel(), rows, cols,
@@ -349,7 +370,8 @@ def gemv_bf16(w: torch.Tensor, x: torch.Tensor, out: torch.Tensor | None = None,
     rows, cols = w.shape
     batch = _batch_of(x, cols)
     if out is None:
-        out = torch.empty((batch, rows), dtype=torch.float32, device=w.device)
+        out = _empty((batch, rows), torch.float32, w.device, stream)
+        _used_on(stream, out)
     _gemv_out(out, batch, rows)
     _same_device("gemv_bf16", w, x, out)
     _check(_lib.wc_gemv_bf16(_ptr(w), rows, cols, _ptr(x), batch, _ptr(out), _stream(stream)),
@@ -490,24 +512,6 @@ def _fp4(q: Fp4, what: str):
             raise ValueError(f"{what}.{name} must be contiguous")
     raise ValueError(f"{what}: codes {tuple(codes.shape)} and scales {tuple(shape)} are not "
                      f"[.., rows, {16 * groups}] and [.., rows, {groups}] of {cols} columns")
-
-
-def _used_on(stream, *tensors):
-    """Memory of another stream's pool that the caller reads on the current
-    stream is not handed out again before that one is done with it."""
-    if stream is not None and stream.cuda_stream != _stream():
-        for t in tensors:
-            t.record_stream(torch.cuda.current_stream())
-
-
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """Memory for a call on `stream` (None: the current one) to write.  It is
-    taken from that stream's pool: what was freed to the current stream's may
-    still be in use by work queued there, which `stream` does not wait for."""
-    if stream is None or stream.cuda_stream == _stream():
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def fp4_encode(w: torch.Tensor, out: Fp4 | None = None, stream=None) -> Fp4:

@@ -26,11 +26,16 @@ Q = wc.fp4_encode(W)
 STACK = [wc.fp4_encode(dev16(synth.random_bits(8 * r * c, 4 + r).reshape(8, r, c)))
          for r, c in ((512, 1024), (1024, 256))]
 TOKENS, ROUTER = dev16(synth.vectors(5, 64, 1024)), dev16(synth.vectors(6, 8, 1024))
+HEAD, CODED = wc.encode(W, wc.BYTESPLIT)
 CALLS = {
     "fp4_encode": lambda s: list(wc.fp4_encode(W, stream=s)[:2]),
     "fp4_decode": lambda s: [wc.fp4_decode(Q, stream=s)],
     "fp4_gemv": lambda s: [wc.fp4_gemv(Q, X, stream=s)],
     "moe": lambda s: list(wc.moe(TOKENS, ROUTER, *STACK, 2, stream=s)),
+    "encode": lambda s: [wc.encode(W, wc.BYTESPLIT, stream=s)[1]],
+    "decode": lambda s: [wc.decode(HEAD, CODED, stream=s)],
+    "decode_gemv": lambda s: [wc.decode_gemv(HEAD, CODED, 1024, 4096, X, stream=s)],
+    "gemv_bf16": lambda s: [wc.gemv_bf16(W, X, stream=s)],
 }
 
 

@@ -21,7 +21,12 @@ class _Lib:
     def __getattr__(self, name):
         if not name.startswith("wc_"):
             raise AttributeError(name)
-        return lambda *args: 4096 if name == "wc_moe_workspace_bytes" else 0
+
+        def call(*args):
+            if name == "wc_build_dict":
+                args[-1]._obj.n, args[-1]._obj.total_bytes = args[2], 2048
+            return 4096 if name == "wc_moe_workspace_bytes" else 0
+        return call
 
 
 @pytest.fixture
@@ -62,12 +67,21 @@ def u8(*shape):
 
 
 W, X, Q = b16(6, 70), b16(3, 70), wc.Fp4(u8(6, 48), u8(6, 3), 70)
+N = 6 * 70
+HEAD, COPY = wc.Header(), u8(2048)
+HEAD.n, HEAD.total_bytes = N, 2048
 MOE = b16(3, 64), b16(5, 64), b16(5, 80, 64), b16(5, 64, 40), 2
 CALLS = {  # the outputs of each call
     "fp4_encode": lambda s: list(wc.fp4_encode(W, stream=s)[:2]),
     "fp4_decode": lambda s: [wc.fp4_decode(Q, stream=s)],
     "fp4_gemv": lambda s: [wc.fp4_gemv(Q, X, stream=s)],
     "moe": lambda s: list(wc.moe(*MOE, stream=s)),
+    "build_dict": lambda s: [wc.build_dict(W, wc.K15, stream=s)][:0],  # a workspace alone
+    "encode_into": lambda s: [wc.encode_into(HEAD, W, COPY, stream=s)][:0],
+    "encode": lambda s: [wc.encode(W, wc.K15, stream=s)[1]],
+    "decode": lambda s: [wc.decode(HEAD, COPY, stream=s)],
+    "decode_gemv": lambda s: [wc.decode_gemv(HEAD, COPY, 6, 70, X, stream=s)],
+    "gemv_bf16": lambda s: [wc.gemv_bf16(W, X, stream=s)],
 }
 
 

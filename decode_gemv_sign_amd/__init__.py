@@ -221,6 +221,20 @@ def _same_device(what: str, *ts: torch.Tensor):
             raise ValueError(f"{what}: tensors on different devices {devs}")
 
 
+def _placed(what: str, stream, *ts: torch.Tensor):
+    """The tensors must be on the current device, where the kernels run, and
+    so must `stream` (None: the current one)."""
+    _same_device(what, *ts)
+    device = ts[0].get_device()
+    if device < 0:  # of no GPU: refused before
+        return
+    here = torch._C._cuda_getDevice()
+    if device != here:
+        raise ValueError(f"{what}: tensors on device {device}, the current device is {here}")
+    if stream is not None and stream.device_index != device:
+        raise ValueError(f"{what}: tensors on device {device}, the stream is on {stream.device_index}")
+
+
 def _batch_of(x: torch.Tensor, cols: int, what: str = "x") -> int:
     """Rows of x, which must be exactly [batch, cols] (or [cols] for batch 1):
     the library reads batch * cols values and cannot check that itself."""
@@ -530,7 +544,7 @@ def fp4_encode(w: torch.Tensor, out: Fp4 | None = None, stream=None) -> Fp4:
         if tuple(out.scales.shape) != (*w.shape[:-1], groups) or out.cols != cols:
             raise ValueError(f"out holds {tuple(out.scales.shape[:-1])} rows of {out.cols} columns, "
                              f"w has shape {tuple(w.shape)}")
-        _same_device("fp4_encode", w, out.codes, out.scales)
+    _placed("fp4_encode", stream, w, out.codes, out.scales)
     _check(_lib.wc_fp4_encode(_ptr(w), w.shape[:-1].numel(), cols, _ptr(out.codes),
                               _ptr(out.scales), _stream(stream)), "wc_fp4_encode")
     return out
@@ -545,7 +559,7 @@ def fp4_decode(q: Fp4, out: torch.Tensor | None = None, stream=None) -> torch.Te
         _used_on(stream, out)
     elif tuple(_bits16(out, "out").shape) != shape:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
-    _same_device("fp4_decode", q.codes, q.scales, out)
+    _placed("fp4_decode", stream, q.codes, q.scales, out)
     _check(_lib.wc_fp4_decode(_ptr(q.codes), _ptr(q.scales), out.shape[:-1].numel(), cols,
                               _ptr(out), _stream(stream)), "wc_fp4_decode")
     return out
@@ -562,7 +576,7 @@ def fp4_gemv(q: Fp4, x: torch.Tensor, out: torch.Tensor | None = None, stream=No
         out = _empty((batch, rows), torch.float32, x.device, stream)
         _used_on(stream, out)
     _gemv_out(out, batch, rows)
-    _same_device("fp4_gemv", q.codes, q.scales, x, out)
+    _placed("fp4_gemv", stream, q.codes, q.scales, x, out)
     _check(_lib.wc_fp4_gemv(_ptr(q.codes), _ptr(q.scales), rows, cols, _ptr(x), batch, _ptr(out),
                             _stream(stream)), "wc_fp4_gemv")
     return out
@@ -646,7 +660,7 @@ def moe(x: torch.Tensor, router: torch.Tensor, gate_up, down, top_k: int, *, sco
     ids = _empty((tokens, top_k), torch.int32, x.device, stream)
     weights = _empty((tokens, top_k), torch.float32, x.device, stream)
     _used_on(stream, ids, weights)
-    _same_device("moe", x, router, work, out, *tgu, *tdn, *(() if bias is None else (bias,)))
+    _placed("moe", stream, x, router, work, out, *tgu, *tdn, *(() if bias is None else (bias,)))
     shape = _moe_shape(tokens, hidden, inter, experts, top_k, scoring, renorm, scale)
     _check(_lib.wc_moe(ctypes.byref(shape), _ptr(x), _ptr(router), _ptr(bias), ctypes.byref(cgu),
                        ctypes.byref(cdn), _ptr(out), _ptr(ids), _ptr(weights), _ptr(work),

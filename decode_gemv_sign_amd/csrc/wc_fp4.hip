@@ -104,7 +104,8 @@ struct Fp4Args {
   const uint8_t* scales;
   const uint16_t* x;
   float* y;
-  uint64_t rows;
+  uint64_t rows;    // of this launch
+  uint64_t stride;  // floats from one input's outputs to the next one's
   uint32_t cols, batch;
 };
 
@@ -177,7 +178,7 @@ __global__ __launch_bounds__(kWave * 16) void k_fp4_gemv(Fp4Args a) {
     if (b < a.batch && !(QUAD && (n & 3u))) {
 #pragma unroll
       for (uint32_t k = 0; k < 4; ++k)
-        if (y0 + k < a.rows) a.y[(uint64_t)b * a.rows + y0 + k] = s[k];
+        if (y0 + k < a.rows) a.y[b * a.stride + y0 + k] = s[k];
     }
   }
 }
@@ -326,7 +327,7 @@ __global__ __launch_bounds__(kWave * kWideWaves) void k_fp4_wide(Fp4Args a) {
     if (b < a.batch) {
 #pragma unroll
       for (uint32_t k = 0; k < 4; ++k)
-        if (y0 + k < a.rows) a.y[(uint64_t)b * a.rows + y0 + k] = s[k];
+        if (y0 + k < a.rows) a.y[b * a.stride + y0 + k] = s[k];
     }
   }
 }
@@ -387,6 +388,20 @@ void launch_wide_for(const Fp4Args& a, hipStream_t s) {
     launch_wide<2, 1, 4>(a, s);
 }
 
+void launch_gemv(const Fp4Args& a, hipStream_t s) {
+  const uint32_t row_blocks = (uint32_t)((a.rows + kRowTile - 1u) / kRowTile);
+  if (a.batch <= 4)
+    launch_rows<true>(a, row_blocks, 1, s);
+  else if (a.cols % 8u || (a.batch <= 16 && wide_blocks(a, 2, 1) < wide_enough()))
+    launch_rows<false>(a, row_blocks, (a.batch + 15u) / 16u, s);
+  else
+    launch_wide_for(a, s);
+}
+
+// Most rows of one launch: a grid has fewer than 2^32 threads in x, and k_fp4_wide of
+// 32 rows takes 8 for a row (k_fp4_gemv, which has one wave per block by then, 4).
+constexpr uint64_t kLaunchRows = 1ull << 28;
+
 uint32_t piece_blocks(uint64_t pieces) {
   const uint64_t b = (pieces + kBlockThreads - 1) / kBlockThreads;
   const uint64_t most = (uint64_t)cu_count() * 16u;
@@ -428,16 +443,12 @@ extern "C" int wc_fp4_gemv(const uint8_t* d_codes, const uint8_t* d_scales, uint
   if (!d_y || ((uintptr_t)d_y & 3u)) return WC_E_ARG;
   if (cols && (!d_codes || !wc::aligned16(d_codes) || !d_scales || !d_x || !wc::aligned16(d_x)))
     return WC_E_ARG;
-  const uint64_t row_blocks = (rows + wc::kRowTile - 1) / wc::kRowTile;
-  if (row_blocks >= (1ull << 31)) return WC_E_SIZE;
-  wc::Fp4Args a = {d_codes, d_scales, d_x, d_y, rows, (uint32_t)cols, batch};
-  hipStream_t s = (hipStream_t)stream;
-  const uint32_t rb = (uint32_t)row_blocks;
-  if (batch <= 4)
-    wc::launch_rows<true>(a, rb, 1, s);
-  else if (cols % 8u || (batch <= 16 && wc::wide_blocks(a, 2, 1) < wc::wide_enough()))
-    wc::launch_rows<false>(a, rb, (batch + 15u) / 16u, s);
-  else
-    wc::launch_wide_for(a, s);
-  return wc::launched();
+  if (rows >= (1ull << 35)) return WC_E_SIZE;  // cols 0
+  for (uint64_t r = 0; r < rows; r += wc::kLaunchRows) {
+    const uint64_t n = rows - r < wc::kLaunchRows ? rows - r : wc::kLaunchRows;
+    wc::launch_gemv({d_codes + WC_FP4_CODE_BYTES(r, cols), d_scales + WC_FP4_SCALE_BYTES(r, cols), d_x,
+                     d_y + r, n, rows, (uint32_t)cols, batch}, (hipStream_t)stream);
+    if (const int v = wc::launched()) return v;
+  }
+  return WC_OK;
 }

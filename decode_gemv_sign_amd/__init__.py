@@ -591,6 +591,10 @@ MOE_MAX_TOKENS = 64
 
 
 def _moe_shape(tokens, hidden, inter, experts, top_k, scoring, renorm, scale) -> MoeShape:
+    for name, v in (("top_k", top_k), ("scoring", scoring), ("tokens", tokens), ("hidden", hidden),
+                    ("inter", inter), ("experts", experts)):
+        if not 0 <= v < 1 << 32:  # ctypes would take it modulo 2^32
+            raise ValueError(f"{name} {v} outside 0..2^32 - 1")
     return MoeShape(tokens, hidden, inter, experts, top_k, scoring, MOE_RENORM if renorm else 0,
                     scale)
 

@@ -441,7 +441,7 @@ extern "C" int wc_fp4_gemv(const uint8_t* d_codes, const uint8_t* d_scales, uint
   if (const int v = wc::fp4_shape_ok(rows, cols)) return v;
   if (rows == 0) return WC_OK;
   if (!d_y || ((uintptr_t)d_y & 3u)) return WC_E_ARG;
-  if (cols && (!d_codes || !wc::aligned16(d_codes) || !d_scales || !d_x || !wc::aligned16(d_x)))
+  if (cols && (!d_codes || !wc::aligned16(d_codes) || !d_scales || !wc::rows_aligned(d_x, cols)))
     return WC_E_ARG;
   if (rows >= (1ull << 35)) return WC_E_SIZE;  // cols 0
   for (uint64_t r = 0; r < rows; r += wc::kLaunchRows) {

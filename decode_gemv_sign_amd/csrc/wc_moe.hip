@@ -784,7 +784,7 @@ extern "C" int wc_moe(const wc_moe_shape* shape, const uint16_t* d_x, const uint
   if (const int v = wc::moe_shape_ok(shape)) return v;
   if (const int v = wc::experts_ok(gate_up)) return v;
   if (const int v = wc::experts_ok(down)) return v;
-  if (!d_x || !wc::aligned16(d_x) || !d_router || !wc::aligned16(d_router)) return WC_E_ARG;
+  if (!wc::rows_aligned(d_x, shape->hidden) || !d_router || !wc::aligned16(d_router)) return WC_E_ARG;
   if (!d_y || ((uintptr_t)d_y & 1u)) return WC_E_ARG;
   if (((uintptr_t)d_bias | (uintptr_t)d_ids | (uintptr_t)d_weights) & 3u) return WC_E_ARG;
   if (!d_work || !wc::aligned16(d_work)) return WC_E_ARG;

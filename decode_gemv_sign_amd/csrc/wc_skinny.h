@@ -82,6 +82,12 @@ __device__ __forceinline__ void each(F&& f) {
   }
 }
 
+// Inputs that the kernels can read: rows that start at 16-byte boundaries, or, of a
+// length that rules this out, at any 2-byte address.
+inline bool rows_aligned(const void* x, uint64_t cols) {
+  return x && ((uintptr_t)x & (cols % 8u ? 1u : 15u)) == 0;
+}
+
 // ---- loads -------------------------------------------------------------------
 
 // Bytes [0, n) from p on (wave-uniform).  What a load asks for past them reads as

@@ -20,8 +20,9 @@
  * Conventions as in wc.h: caller-owned device memory, work enqueued on
  * `stream` in order without waiting, WC_OK or a negative WC_E_* code, nothing
  * enqueued when an argument check fails, no abort and no exception.
- * d_w, d_out, d_x and d_codes must be 16-byte aligned, d_y 4-byte; d_scales
- * may have any alignment.
+ * d_w, d_out and d_codes must be 16-byte aligned, d_x too when cols is a
+ * multiple of 8 and 2-byte otherwise, d_y 4-byte; d_scales may have any
+ * alignment.
  */
 #ifndef WC_FP4_H
 #define WC_FP4_H

@@ -22,8 +22,9 @@
  * BF16 once at the end.  The sums'
  * order is fixed by the shape: the same call gives the same bits.
  *
- * Conventions as in wc.h.  d_x, d_router, the weights' d_data and d_work are
- * 16-byte aligned, d_y 2-byte, d_bias, d_ids and d_weights 4-byte.
+ * Conventions as in wc.h.  d_router, the weights' d_data and d_work are 16-byte
+ * aligned, d_x too when hidden is a multiple of 8 and 2-byte otherwise, d_y
+ * 2-byte, d_bias, d_ids and d_weights 4-byte.
  */
 #ifndef WC_MOE_H
 #define WC_MOE_H

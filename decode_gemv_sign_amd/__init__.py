@@ -494,8 +494,7 @@ def artifact_verify(path: str, device="cuda:0"):
 
 # ---- 4-bit weights with group scales (include/wc_fp4.h) ----------------------
 
-FP4_GROUP = 32          # columns that share a scale
-FP4_MAX_COLS = 1 << 24  # WC_FP4_MAX_COLS
+FP4_GROUP = 32  # columns that share a scale
 
 
 class Fp4(NamedTuple):

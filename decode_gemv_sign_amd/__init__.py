@@ -151,6 +151,7 @@ def use_library(path: str):
     """Bind this module to another build of libwc (e.g. a tuning variant)."""
     global _lib
     _lib = _load(path)
+    moe_workspace_bytes.cache_clear()  # another build may lay its workspace out otherwise
 
 
 def _check(st: int, what: str):

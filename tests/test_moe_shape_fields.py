@@ -1,5 +1,6 @@
 """Numbers that do not fit a field of wc_moe_shape are refused: they are not
-taken modulo 2^32, which would make another layer of them."""
+taken modulo 2^32, which would make another layer of them.  The workspace's size
+is that of the library in use."""
 import pytest
 import torch
 
@@ -47,3 +48,20 @@ def test_workspace_refuses(at, wrap):
     shape[at] += wrap
     with pytest.raises(ValueError, match="outside"):
         wc.moe_workspace_bytes(*shape)
+
+
+def test_workspace_size_follows_the_library(monkeypatch):
+    class Other:
+        @staticmethod
+        def wc_moe_workspace_bytes(shape):
+            return 12345
+
+    here, lib = wc.moe_workspace_bytes(3, 64, 40, 5, 2), wc._lib
+    assert here != 12345
+    monkeypatch.setattr(wc, "_load", lambda path: Other if path == "other" else lib)
+    try:
+        wc.use_library("other")
+        assert wc.moe_workspace_bytes(3, 64, 40, 5, 2) == 12345
+    finally:
+        wc.use_library(wc.LIB_PATH)
+    assert wc.moe_workspace_bytes(3, 64, 40, 5, 2) == here and wc._lib is lib

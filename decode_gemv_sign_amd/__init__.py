@@ -151,7 +151,6 @@ def use_library(path: str):
     """Bind this module to another build of libwc (e.g. a tuning variant)."""
     global _lib
     _lib = _load(path)
-    moe_workspace_bytes.cache_clear()  # another build may lay its workspace out otherwise
 
 
 def _check(st: int, what: str):
@@ -600,10 +599,15 @@ def _moe_shape(tokens, hidden, inter, experts, top_k, scoring, renorm, scale) ->
 
 
 @functools.lru_cache(maxsize=256)
-def moe_workspace_bytes(tokens: int, hidden: int, inter: int, experts: int, top_k: int) -> int:
-    """wc_moe_workspace_bytes: device scratch of one moe call of that shape."""
-    need = _lib.wc_moe_workspace_bytes(
+def _moe_need(lib, tokens, hidden, inter, experts, top_k) -> int:
+    return lib.wc_moe_workspace_bytes(
         ctypes.byref(_moe_shape(tokens, hidden, inter, experts, top_k, SOFTMAX, True, 1.0)))
+
+
+def moe_workspace_bytes(tokens: int, hidden: int, inter: int, experts: int, top_k: int) -> int:
+    """wc_moe_workspace_bytes: device scratch of one moe call of that shape
+    (looked up once for each library and shape)."""
+    need = _moe_need(_lib, tokens, hidden, inter, experts, top_k)
     if need == 0:
         raise WCError(-5, "wc_moe_workspace_bytes")
     return need

@@ -46,10 +46,10 @@ __device__ inline uint32_t max_abs8(u32x4 w) {
 
 // A lane codes 8 columns; the four lanes of a group share their maximum.
 // Blocks walk the rows' pieces of 8 columns, 4 G per row.  Bound by HBM:
-// 24576 x 6144 in 69 us, 382 MB at 5.5 TB/s (a plain copy of 2 GiB: 4.9); 96 us with
-// loads that leave the weights, which nothing reads again, in the caches, and 107
-// with four of those in flight per lane.  1000 x 4100: 4.4 us, of which 2.4 are an
-// empty kernel's.
+// 24576 x 6144 in 66 us, 382 MB at 5.8 TB/s (a plain copy of 2 GiB: 4.9); 73 us with
+// loads that leave the weights, which nothing reads again, in the caches.  Four loads
+// in flight per lane took longer.  1000 x 4100: 4.2 us, of which 2.4 are an empty
+// kernel's.
 __global__ __launch_bounds__(kBlockThreads) void k_fp4_encode(const uint16_t* __restrict__ w,
                                                               uint64_t rows, uint32_t cols,
                                                               uint32_t groups,
@@ -75,8 +75,9 @@ __global__ __launch_bounds__(kBlockThreads) void k_fp4_encode(const uint16_t* __
   }
 }
 
-// A lane rebuilds 8 columns.  Bound by HBM: 24576 x 6144 in 57 us, 387 MB
-// at 6.8 TB/s (65 with stores that stay in the caches).
+// A lane rebuilds 8 columns.  Bound by HBM: 24576 x 6144 in 72 us with all 387 MB to and
+// from there, 5.4 TB/s (75 with stores that stay in the caches); 57 right after
+// k_fp4_encode, whose codes are then still in the memory-side cache.  1000 x 4100: 4.0 us.
 __global__ __launch_bounds__(kBlockThreads) void k_fp4_decode(const uint8_t* __restrict__ codes,
                                                               const uint8_t* __restrict__ scales,
                                                               uint64_t rows, uint32_t cols,
@@ -116,13 +117,16 @@ struct Fp4Args {
 // of the steps, and their sums are added in LDS in wave order.  Input rows past
 // the batch repeat the last one and are not stored.  ANY: rows of inputs that do
 // not start at 16-byte boundaries.
-// At one to four inputs it is bound by HBM: 24576 x 6144, batch 1: 80 MB in 16.5 us,
-// 4.9 TB/s (6.2 is the most a read-only kernel reached from HBM); 14336 x 4096,
-// batch 4: 32 MB in 8.5 us, of which 2.4 are an empty kernel's.  A small call is
-// launch and one trip to memory: 1024 x 4096 in 3.7 us.  At 5 to 16 the inputs'
-// loads and their transposition count as much as the codes: 5003 x 4100, batch 16:
-// 10.2 us.  Loading several steps at once, or as a pipeline, took longer at every
-// size: the loads are bound by their address cycles, not by their latency.
+// At one to four inputs it is bound by memory.  24576 x 6144, batch 1: 80 MB from HBM in
+// 20.5 us, 3.9 TB/s (6.2 is the most a read-only kernel reached from there); 17 where
+// the memory-side cache holds them (three such matrices in turn).  14336 x 4096, batch 4:
+// 32 MB in 10.1 us, cached 8.4, of which 2.4 are an empty kernel's.  A small call is
+// launch and one trip to memory: 1024 x 4096 in 4.2 us, cached 3.7.  At 5 to 16 the
+// inputs' loads and their transposition count as much as the codes: 5003 rows, batch
+// 16: 4096 columns 8.9 us, 4104 (a short last step) 10.6, 4100 (rows at 8-byte
+// boundaries besides) 11.9, 4101 13.6; cached 7.2, 8.5, 10.3 and 11.9.  Loading several
+// steps at once, or as a pipeline, took longer at every size: the loads are bound by
+// their address cycles, not by their latency.
 template <bool QUAD, bool ANY>
 __global__ __launch_bounds__(kWave * 16) void k_fp4_gemv(Fp4Args a) {
   extern __shared__ mfma_f32x4 part[];  // [waves][kWave]
@@ -195,10 +199,12 @@ __global__ __launch_bounds__(kWave * 16) void k_fp4_gemv(Fp4Args a) {
 // take one, as LDS has to hold two such blocks per compute unit (24576 x 6144,
 // batch 64: 43.9 against 48.6).  Nothing is shared between waves until the end, so
 // there is no barrier for their loads to wait at.
-// 6144 x 24576, batch 32: 83 MB in 28.6 to 32 us; without the inputs' loads it took
-// 22, without the codes' 31, without the products as long: it waits for the inputs,
-// 1.5 MB from L2 per compute unit.  4096 x 4096, batch 256: 17.5 us, 490 TFLOP/s, of
-// which the blocks' first loads and the launch are about 5.
+// 6144 x 24576, batch 32: 83 MB in 28 to 33 us where the memory-side cache holds the
+// codes, 38 from HBM.  Without the inputs' loads it took 22 (cached), without the
+// codes' 31, without the products as long: it waits for the inputs, 1.5 MB from L2 per
+// compute unit, and its 192 blocks leave a quarter of the units idle.  4096 x 4096,
+// batch 256: 18.6 us, 460 TFLOP/s, of which the blocks' first loads and the launch are
+// about 5.
 constexpr uint32_t kWideLoad = 1024u + 16u;
 constexpr uint32_t kWideWaves = 4;
 

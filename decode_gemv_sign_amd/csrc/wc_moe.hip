@@ -414,11 +414,12 @@ __device__ inline void choose_all(const MoeArgs& a, MoeChoice& c, MoeRoute* rout
 // The weights of experts with one unit of tokens pass the caches by; those of more
 // units do not, as the next tile reads them again (64 tokens, 8 experts of 2048 x 4096,
 // 2 each: 122 us for the layer, 129 if they do).
-// Bound by HBM where there are many weights: BF16, 32 experts of 2048 x 4096, 2
-// tokens, 4 each: 252 MB in 46 us, 5.5 TB/s; 64 experts of 1024 x 2048, 64 tokens: 537
-// MB in 100 us, 5.4 TB/s; 4-bit, 128 experts of 1024 x 4096, 16 tokens: 365 MB in 71 us,
-// 5.1 TB/s.  One token of 64 experts of 1408 x 2048, 4-bit: 18 MB in 14 us, most of it
-// the launch, the choice and the inputs before the first product.
+// Bound by HBM where there are many weights (bytes fetched, by the counters): BF16, 32
+// experts of 2048 x 4096, 2 tokens, 4 each: 235 MB in 46 us, 5.1 TB/s; 64 experts of
+// 1024 x 2048, 64 tokens: 540 MB in 100 us, 5.4 TB/s; 4-bit, 128 experts of 1024 x 4096,
+// 16 tokens: 343 MB in 68 us, 5.1 TB/s.  One token of 64 experts of 1408 x 2048, 4-bit:
+// 19 MB in 14 us, most of it the launch, the choice, which every block makes before its
+// first load of weights, and the inputs.
 template <int KIND>
 __global__ __launch_bounds__(kWave * kUpWaves, 3) void k_moe_gate_up(MoeArgs a) {
   __shared__ MoeChoice c;
@@ -608,8 +609,8 @@ __global__ __launch_bounds__(kWave * kUpWaves, 3) void k_moe_gate_up(MoeArgs a) 
 // n & 7 of the unit, or (n >= 8) the low part.  When a unit is done, its sums go to
 // the wave's own [token][16] array in LDS; at the end these are added over the
 // waves, and over the parts by the last block to arrive, in order both.
-// BF16, 2 tokens as above: 126 MB in 21.4 us, 5.9 TB/s; 4-bit, 16 tokens: 182 MB in 39 to
-// 47 us; one token: 9 MB in 7 us.  12 waves took the same as 16; the
+// BF16, 2 tokens as above: 118 MB fetched in 21.3 us, 5.6 TB/s; 4-bit, 16 tokens: 174 MB
+// in 38 to 44 us; one token: 10 MB in 7.7 us.  12 waves took the same as 16; the
 // operands of the activations loaded by quads and transposed here instead of stored
 // in operand order by k_moe_gate_up spilled registers and took longer.
 template <int KIND, int U>

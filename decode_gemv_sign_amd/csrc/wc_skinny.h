@@ -201,8 +201,10 @@ struct WeightStep {
 // TAIL: the row's last step, of which some columns do not exist: they read as 0.
 // ONCE: for weights that no other tile of inputs needs.  It pays in the MoE
 // kernels, where an expert's matrices are one tile's (128 experts, 16 tokens, 4-bit:
-// 139 -> 124 us; 32 experts, BF16, 2 tokens: 80 -> 73.5); the 4-bit GEMV took longer with it
-// (24576 x 6144, batch 1: 16.4 -> 18.2).
+// 127 us without, 114 with; 32 experts, BF16, 2 tokens: 81 and 75; 64 experts, BF16,
+// 64 tokens: 170 and 157).  The 4-bit GEMV goes without: its matrices may still be in
+// the card's memory-side cache (24576 x 6144, batch 1: 17.6 us without, 18.5 with;
+// from HBM 20.4 and 19.0).
 template <int KIND, bool TAIL, bool ONCE = false>
 __device__ __forceinline__ void load_weights(const WeightLane<KIND>& l, const WeightTile<KIND>& w,
                                              uint32_t step, WeightStep& s) {

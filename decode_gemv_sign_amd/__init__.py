@@ -166,22 +166,25 @@ def _stream(stream=None) -> int:
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
-def _used_on(stream, *tensors):
+def _used_on(*tensors):
     """Memory of another stream's pool that the caller reads on the current
     stream is not handed out again before that one is done with it."""
-    if stream is not None and stream.cuda_stream != _stream():
-        for t in tensors:
-            t.record_stream(torch.cuda.current_stream())
+    for t in tensors:
+        t.record_stream(torch.cuda.current_stream())
 
 
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """Memory for a call on `stream` (None: the current one) to write.  It is
-    taken from that stream's pool: what was freed to the current stream's may
-    still be in use by work queued there, which `stream` does not wait for."""
+def _empty(shape, dtype, device, stream, returned: bool = True) -> torch.Tensor:
+    """Memory for a call on `stream` (None: the current one) to write, and for
+    the caller to read if `returned`.  It is taken from that stream's pool: what
+    was freed to the current stream's may still be in use by work queued there,
+    which `stream` does not wait for."""
     if stream is None or stream.cuda_stream == _stream():
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        _used_on(t)
+    return t
 
 
 def _on_device(t: torch.Tensor) -> bool:
@@ -224,8 +227,10 @@ def _same_device(what: str, *ts: torch.Tensor):
 def _placed(what: str, stream, *ts: torch.Tensor):
     """The tensors must be on the current device, where the kernels run, and
     so must `stream` (None: the current one)."""
-    _same_device(what, *ts)
     device = ts[0].get_device()
+    for t in ts:
+        if t.get_device() != device:
+            _same_device(what, *ts)
     if device < 0:  # of no GPU: refused before
         return
     here = torch._C._cuda_getDevice()
@@ -275,7 +280,7 @@ def workspace_bytes(n: int) -> int:
 
 
 def _workspace(n: int, device, stream) -> torch.Tensor:
-    return _empty(workspace_bytes(n), torch.uint8, device, stream)
+    return _empty(workspace_bytes(n), torch.uint8, device, stream, returned=False)
 
 
 def build_dict(w: torch.Tensor, layout: int, work: torch.Tensor | None = None,
@@ -330,7 +335,6 @@ def encode(w: torch.Tensor, layout: int, stream=None):
     work = _workspace(w.numel(), w.device, stream)
     h = build_dict(w, layout, work, stream)
     c = _empty(h.total_bytes, torch.uint8, w.device, stream)
-    _used_on(stream, c)
     encode_into(h, w, c, work, stream)
     return h, c
 
@@ -346,7 +350,6 @@ def decode(h: Header, container: torch.Tensor, out: torch.Tensor | None = None,
     _bytes(container, "container", h.total_bytes)
     if out is None:
         out = _empty(h.n, torch.int16, container.device, stream)
-        _used_on(stream, out)
     out = _bits16(out, "out")
     if out.numel() < h.n:
         raise ValueError(f"out holds {out.numel()} weights, {h.n} needed")
@@ -366,7 +369,6 @@ def decode_gemv(h: Header, container: torch.Tensor, rows: int, cols: int, x: tor
     batch = _batch_of(x, cols)
     if out is None:
         out = _empty((batch, rows), torch.float32, container.device, stream)
-        _used_on(stream, out)
     _gemv_out(out, batch, rows)
     _same_device("decode_gemv", container, x, out)
     _check(_lib.wc_decode_gemv(ctypes.byref(h), _ptr(container), container.numel(), rows, cols,
@@ -385,7 +387,6 @@ def gemv_bf16(w: torch.Tensor, x: torch.Tensor, out: torch.Tensor | None = None,
     batch = _batch_of(x, cols)
     if out is None:
         out = _empty((batch, rows), torch.float32, w.device, stream)
-        _used_on(stream, out)
     _gemv_out(out, batch, rows)
     _same_device("gemv_bf16", w, x, out)
     _check(_lib.wc_gemv_bf16(_ptr(w), rows, cols, _ptr(x), batch, _ptr(out), _stream(stream)),
@@ -535,15 +536,15 @@ def fp4_encode(w: torch.Tensor, out: Fp4 | None = None, stream=None) -> Fp4:
     cols = w.shape[-1]
     groups = (cols + FP4_GROUP - 1) // FP4_GROUP
     if out is None:
+        _placed("fp4_encode", stream, w)
         out = Fp4(_empty((*w.shape[:-1], 16 * groups), torch.uint8, w.device, stream),
                   _empty((*w.shape[:-1], groups), torch.uint8, w.device, stream), cols)
-        _used_on(stream, out.codes, out.scales)
     else:
         _fp4(out, "out")
         if tuple(out.scales.shape) != (*w.shape[:-1], groups) or out.cols != cols:
             raise ValueError(f"out holds {tuple(out.scales.shape[:-1])} rows of {out.cols} columns, "
                              f"w has shape {tuple(w.shape)}")
-    _placed("fp4_encode", stream, w, out.codes, out.scales)
+        _placed("fp4_encode", stream, w, out.codes, out.scales)
     _check(_lib.wc_fp4_encode(_ptr(w), w.shape[:-1].numel(), cols, _ptr(out.codes),
                               _ptr(out.scales), _stream(stream)), "wc_fp4_encode")
     return out
@@ -555,7 +556,6 @@ def fp4_decode(q: Fp4, out: torch.Tensor | None = None, stream=None) -> torch.Te
     shape = (*lead, rows, cols)
     if out is None:
         out = _empty(shape, torch.bfloat16, q.codes.device, stream)
-        _used_on(stream, out)
     elif tuple(_bits16(out, "out").shape) != shape:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
     _placed("fp4_decode", stream, q.codes, q.scales, out)
@@ -573,7 +573,6 @@ def fp4_gemv(q: Fp4, x: torch.Tensor, out: torch.Tensor | None = None, stream=No
     batch = _batch_of(x, cols)
     if out is None:
         out = _empty((batch, rows), torch.float32, x.device, stream)
-        _used_on(stream, out)
     _gemv_out(out, batch, rows)
     _placed("fp4_gemv", stream, q.codes, q.scales, x, out)
     _check(_lib.wc_fp4_gemv(_ptr(q.codes), _ptr(q.scales), rows, cols, _ptr(x), batch, _ptr(out),
@@ -590,10 +589,9 @@ MOE_MAX_TOKENS = 64
 
 
 def _moe_shape(tokens, hidden, inter, experts, top_k, scoring, renorm, scale) -> MoeShape:
-    for name, v in (("top_k", top_k), ("scoring", scoring), ("tokens", tokens), ("hidden", hidden),
-                    ("inter", inter), ("experts", experts)):
-        if not 0 <= v < 1 << 32:  # ctypes would take it modulo 2^32
-            raise ValueError(f"{name} {v} outside 0..2^32 - 1")
+    if (tokens | hidden | inter | experts | top_k | scoring) >> 32:  # ctypes would take it modulo 2^32
+        raise ValueError(f"tokens {tokens}, hidden {hidden}, inter {inter}, experts {experts}, top_k {top_k}, "
+                         f"scoring {scoring}: one is outside 0..2^32 - 1")
     return MoeShape(tokens, hidden, inter, experts, top_k, scoring, MOE_RENORM if renorm else 0,
                     scale)
 
@@ -658,16 +656,14 @@ def moe(x: torch.Tensor, router: torch.Tensor, gate_up, down, top_k: int, *, sco
             raise ValueError(f"bias must be a contiguous [{experts}], got {tuple(bias.shape)}")
     need = moe_workspace_bytes(tokens, hidden, inter, experts, top_k)
     if work is None:
-        work = _empty(need, torch.uint8, x.device, stream)
+        work = _empty(need, torch.uint8, x.device, stream, returned=False)
     _bytes(work, "work", need)
     if out is None:
         out = _empty((tokens, hidden), torch.bfloat16, x.device, stream)
-        _used_on(stream, out)
     if tuple(_bits16(out, "out").shape) != (tokens, hidden):
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(tokens, hidden)}")
     ids = _empty((tokens, top_k), torch.int32, x.device, stream)
     weights = _empty((tokens, top_k), torch.float32, x.device, stream)
-    _used_on(stream, ids, weights)
     _placed("moe", stream, x, router, work, out, *tgu, *tdn, *(() if bias is None else (bias,)))
     shape = _moe_shape(tokens, hidden, inter, experts, top_k, scoring, renorm, scale)
     _check(_lib.wc_moe(ctypes.byref(shape), _ptr(x), _ptr(router), _ptr(bias), ctypes.byref(cgu),

@@ -180,6 +180,8 @@ def _empty(shape, dtype, device, stream, returned: bool = True) -> torch.Tensor:
     which `stream` does not wait for."""
     if stream is None or stream.cuda_stream == _stream():
         return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "device_index"):  # not torch's: an object with the handle alone
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
     if returned:
@@ -236,7 +238,7 @@ def _placed(what: str, stream, *ts: torch.Tensor):
     here = torch._C._cuda_getDevice()
     if device != here:
         raise ValueError(f"{what}: tensors on device {device}, the current device is {here}")
-    if stream is not None and stream.device_index != device:
+    if stream is not None and getattr(stream, "device_index", device) != device:
         raise ValueError(f"{what}: tensors on device {device}, the stream is on {stream.device_index}")
 
 

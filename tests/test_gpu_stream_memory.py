@@ -73,3 +73,38 @@ def test_what_the_current_stream_reads_stays(name):
     assert all(bool((t == 3).all()) for t in late)
     assert all(torch.equal(a, b) for a, b in zip(read, ref))
     assert all(torch.equal(a, b) for a, b in zip(again, ref))
+
+
+@pytest.mark.parametrize("name", ["fp4_decode", "fp4_encode", "fp4_gemv", "moe", "decode", "decode_gemv", "gemv_bf16"])
+def test_on_a_joined_stream_of_a_graph(name):
+    """A captured call on another stream, joined to the captured one: replays
+    give the eager bits, with eager calls on that stream in between."""
+    call, side = CALLS[name], torch.cuda.Stream()
+    ref = [t.clone() for t in call(None)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(4):
+        for t in got:
+            t.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        other = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+        assert all(torch.equal(a, b) for a, b in zip(other, ref))
+
+
+def test_a_stream_that_is_a_handle_alone():
+    class Handle:
+        cuda_stream = torch.cuda.Stream().cuda_stream
+
+    torch.cuda.synchronize()
+    for name, call in CALLS.items():
+        got = call(Handle)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, call(None))), name

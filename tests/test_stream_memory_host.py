@@ -12,9 +12,15 @@ META = torch.device("meta")
 HERE, SIDE = 3, 7  # handles of the current and of the other stream
 
 
-class _Stream:
-    def __init__(self, handle):
+class _Handle:
+    """A stream that is not torch's own."""
+
+    def __init__(self, handle, device=None):
         self.cuda_stream = handle
+
+
+class _Stream(_Handle):
+    device_index = 0
 
 
 class _Lib:
@@ -38,6 +44,7 @@ def record(monkeypatch):
 
     @contextlib.contextmanager
     def stream(s):
+        assert isinstance(s, _Stream)
         now.append(s.cuda_stream)
         yield
         now.pop()
@@ -52,6 +59,7 @@ def record(monkeypatch):
     monkeypatch.setattr(wc, "_ptr", lambda t: None)
     monkeypatch.setattr(wc, "_stream", lambda s=None: now[-1] if s is None else s.cuda_stream)
     monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", _Stream)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: _Stream(now[-1]))
     monkeypatch.setattr(torch, "empty", alloc)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: kept.append((s.cuda_stream, t)))
@@ -86,16 +94,17 @@ CALLS = {  # the outputs of each call
 
 
 @pytest.mark.parametrize("name", sorted(CALLS))
-def test_memory_comes_from_the_streams_pool(record, name):
+@pytest.mark.parametrize("kind", [_Stream, _Handle])
+def test_memory_comes_from_the_streams_pool(record, name, kind):
     made, kept = record
-    out = CALLS[name](_Stream(SIDE))
+    out = CALLS[name](kind(SIDE))
     assert made and all(h == SIDE for h, _ in made)
     assert all(any(t is o for _, t in made) for o in out)
     assert all(any(t is o and h == HERE for h, t in kept) for o in out)
 
 
 @pytest.mark.parametrize("name", sorted(CALLS))
-@pytest.mark.parametrize("stream", [None, _Stream(HERE)])
+@pytest.mark.parametrize("stream", [None, _Stream(HERE), _Handle(HERE)])
 def test_memory_of_the_current_stream(record, name, stream):
     made, kept = record
     CALLS[name](stream)

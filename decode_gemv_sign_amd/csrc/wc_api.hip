@@ -123,6 +123,19 @@ extern "C" int wc_decode(const wc_header* h, const uint8_t* d_container, size_t 
   return hip_status(wc::launch_decode(*h, d_container, d_out, (hipStream_t)stream));
 }
 
+namespace {
+
+// Rows that the GEMV kernels' grids take.  A grid has fewer than 2^32 threads (the
+// runtime takes more modulo 2^32 and reports nothing): a wave for a row where rows are
+// no whole groups of 8, else 16 threads for one at most where rows are this many, and a
+// thread for an output where the rows are empty; in whole blocks.
+bool grid_fits(uint64_t rows, uint64_t cols, uint32_t batch) {
+  if (cols == 0) return rows <= ((1ull << 32) - 256u) / batch;
+  return rows <= (cols % 8u ? 1ull << 26 : 1ull << 28) - 16u;
+}
+
+}  // namespace
+
 extern "C" int wc_decode_gemv(const wc_header* h, const uint8_t* d_container,
                               size_t container_bytes, uint64_t rows, uint64_t cols,
                               const uint16_t* d_x, uint32_t batch, float* d_y, void* stream) {
@@ -133,6 +146,7 @@ extern "C" int wc_decode_gemv(const wc_header* h, const uint8_t* d_container,
   if (batch < 1 || batch > WC_MAX_BATCH) return WC_E_UNSUPPORTED;
   if (cols && rows > h->n / cols) return WC_E_ARG;
   if (rows * cols != h->n) return WC_E_ARG;
+  if (!grid_fits(rows, cols, batch)) return WC_E_SIZE;
   if (rows && (!d_y || ((uintptr_t)d_y & 3u))) return WC_E_ARG;
   if (rows && cols && (!d_x || !wc::aligned16(d_x))) return WC_E_ARG;
   return hip_status(
@@ -142,7 +156,7 @@ extern "C" int wc_decode_gemv(const wc_header* h, const uint8_t* d_container,
 extern "C" int wc_gemv_bf16(const uint16_t* d_w, uint64_t rows, uint64_t cols, const uint16_t* d_x,
                             uint32_t batch, float* d_y, void* stream) {
   if (batch < 1 || batch > WC_MAX_BATCH) return WC_E_UNSUPPORTED;
-  if (cols && rows >= (1ull << 62) / cols) return WC_E_SIZE;
+  if ((cols && rows >= (1ull << 62) / cols) || !grid_fits(rows, cols, batch)) return WC_E_SIZE;
   if (rows && (!d_y || ((uintptr_t)d_y & 3u))) return WC_E_ARG;
   if (rows && cols && (!d_w || !d_x || !wc::aligned16(d_w) || !wc::aligned16(d_x))) return WC_E_ARG;
   return hip_status(wc::launch_gemv_bf16(d_w, rows, cols, d_x, batch, d_y, (hipStream_t)stream));

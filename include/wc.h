@@ -79,7 +79,7 @@ extern "C" {
 
 #define WC_OK 0
 #define WC_E_ARG (-1)         /* null pointer, misalignment, bad size/shape */
-#define WC_E_SIZE (-2)        /* n >= 2^32, or a buffer smaller than needed */
+#define WC_E_SIZE (-2)        /* n >= 2^32, too many rows, or a buffer smaller than needed */
 #define WC_E_CORRUPT (-3)     /* header fails validation */
 #define WC_E_HIP (-4)         /* a HIP call or kernel launch failed */
 #define WC_E_UNSUPPORTED (-5) /* batch outside 1..WC_MAX_BATCH */
@@ -205,7 +205,9 @@ int wc_decode(const wc_header *h, const uint8_t *d_container,
  * encaja con los sistemas anteriores?"], each rebuilt weight is used by up
  * to 128 input rows on the matrix cores: above 32 input rows (above 16 on
  * tensors of 2^26 weights or more) when cols is a multiple of 128.  Other
- * batches above 16 run 16 input rows at a time.  Both escape forms are
+ * batches above 16 run 16 input rows at a time.  Rows: at most 2^28 - 16,
+ * 2^26 - 16 where cols is not a multiple of 8, (2^32 - 256) / batch where cols
+ * is 0 (WC_E_SIZE).  Both escape forms are
  * taken; in the compact one (WC_FLAG_COMPACT) a row that starts inside an
  * index tile finds its first record by counting the code-15 marks from the
  * tile start.
@@ -218,7 +220,8 @@ int wc_decode_gemv(const wc_header *h, const uint8_t *d_container,
 /*
  * Plain BF16 GEMV, the comparison the pages time the fused kernel against
  * [P3 "Qué queda por demostrar"]: same shapes, types and reduction tree as
- * wc_decode_gemv, with W read as uncompressed BF16 [rows][cols].
+ * wc_decode_gemv, with W read as uncompressed BF16 [rows][cols]; the same
+ * limits of rows.
  */
 int wc_gemv_bf16(const uint16_t *d_w, uint64_t rows, uint64_t cols,
                  const uint16_t *d_x, uint32_t batch, float *d_y, void *stream);

@@ -28,9 +28,11 @@ TILE = 32   # tokens of a tile of the cache
 def listed():
     return [
         # one decode step of a batch: latency counts
-        {"name": "append 32 tokens", "op": "append", "tokens": 32, "kv_heads": 8, "dim": 128, "page": 64},
+        {"name": "append 32 tokens", "op": "append", "tokens": 32, "run": 1, "kv_heads": 8, "dim": 128,
+         "page": 64},
         # the keys and values of a prompt, as slices of the fused projection's output
-        {"name": "append 8192 tokens", "op": "append", "tokens": 8192, "kv_heads": 8, "dim": 128, "page": 64},
+        {"name": "append 8192 tokens", "op": "append", "tokens": 8192, "run": 64, "kv_heads": 8, "dim": 128,
+         "page": 64},
         # one sequence, one token: latency counts
         {"name": "cache b1 1500", "op": "cache", "batch": 1, "new": 1, "longest": 1500, "spread": 1, "heads": 32,
          "kv_heads": 8, "dim": 128, "page": 64, "window": 0},
@@ -84,6 +86,7 @@ def draw(rng):
         if op == "append":
             c = {"op": op, "tokens": _spread(rng, 1, 8192), "kv_heads": kv, "dim": dim,
                  "page": rng.choice((32, 64, 128, 256))}
+            c["run"] = rng.choice((1, rng.randint(1, c["page"]), c["page"]))
         elif op == "cache":
             c = {"op": op, "batch": _spread(rng, 1, 64), "new": rng.choice((1, 1, 1, 2, 5, 8, 16)),
                  "longest": _spread(rng, 1, 65536), "spread": _spread(rng, 1, 100), "heads": heads, "kv_heads": kv,
@@ -344,12 +347,15 @@ def prepare(case, seed):
     s["scale"] = d ** -0.5
     if case["op"] == "append":
         t, page = case["tokens"], case["page"]
-        pages = -(-t // page) + 8
+        runs = -(-t // case["run"])  # of consecutive slots, each somewhere in a page of its own
+        pages = runs + 8
         # slices of one projection's output, whose rows hold two query heads for a head of keys
         fused = keys(t, 4 * h, d)
         s["k"], s["v"] = fused[:, 2 * h:3 * h], fused[:, 3 * h:]
         s["slot_count"] = pages * page
-        s["slots"] = torch.randperm(pages * page, generator=g, device=DEV)[:t]
+        first = torch.randint(page - case["run"] + 1, (runs,), generator=g, device=DEV)
+        first += torch.randperm(pages, generator=g, device=DEV)[:runs] * page
+        s["slots"] = (first[:, None] + torch.arange(case["run"], device=DEV)).flatten()[:t]
         s["cache"] = torch.zeros(pages, h, page // TILE, 34 * d, dtype=torch.uint8, device=DEV)
         return s
     lens, hq = lengths(case), case["heads"]

@@ -11,8 +11,10 @@ de un LLM?").
 
 Next to it a 4-bit tier that loses precision, for tensors that 12 bits per
 weight leave too large (fp4_encode, fp4_decode, fp4_gemv; include/wc_fp4.h),
-and a mixture-of-experts layer for a few tokens on BF16 or 4-bit experts
-(moe; include/wc_moe.h).
+a mixture-of-experts layer for a few tokens on BF16 or 4-bit experts
+(moe; include/wc_moe.h), and a cache of keys and values in the same 4-bit form
+with the attention over it (fp4_cache, fp4_cache_append, fp4_cache_read,
+fp4_attention; include/wc_attn.h).
 
 This module only marshals arguments: every step runs in the HIP kernels of
 libwc.so, on the caller's current torch stream.  PyTorch provides device
@@ -34,6 +36,7 @@ __all__ = [
     "crc32", "container_crcs", "artifact_write", "artifact_entries", "artifact_read",
     "artifact_verify", "LIB_PATH",
     "Fp4", "fp4_encode", "fp4_decode", "fp4_gemv", "SOFTMAX", "SIGMOID", "moe", "moe_workspace_bytes",
+    "fp4_cache", "fp4_cache_append", "fp4_cache_read", "fp4_attention", "fp4_attention_workspace_bytes",
 ]
 
 BYTESPLIT = 0
@@ -102,6 +105,19 @@ class MoeExperts(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_uint32), ("data", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
+class CacheStruct(ctypes.Structure):
+    """wc_fp4_cache (include/wc_attn.h)."""
+    _fields_ = [("data", ctypes.c_void_p), ("pages", ctypes.c_uint64)] + [
+        (n, ctypes.c_uint32) for n in ("page_size", "kv_heads", "head_dim")]
+
+
+class AttentionShape(ctypes.Structure):
+    """wc_fp4_attention_shape (include/wc_attn.h)."""
+    _fields_ = [("q_stride", ctypes.c_uint64)] + [
+        (n, ctypes.c_uint32) for n in ("seqs", "new_tokens", "heads", "table_width", "window")] + [
+        ("scale", ctypes.c_float)]
+
+
 def _load(path: str = LIB_PATH):
     if not os.path.exists(path):
         raise ImportError(
@@ -135,7 +151,13 @@ def _load(path: str = LIB_PATH):
     lib.wc_moe_workspace_bytes.restype = ctypes.c_size_t
     EP = ctypes.POINTER(MoeExperts)
     lib.wc_moe.argtypes = [ctypes.POINTER(MoeShape), P, P, P, EP, EP, P, P, P, P, ctypes.c_size_t, P]
-    for f in (lib.wc_fp4_encode, lib.wc_fp4_decode, lib.wc_fp4_gemv, lib.wc_moe,
+    CP, AP = ctypes.POINTER(CacheStruct), ctypes.POINTER(AttentionShape)
+    lib.wc_fp4_cache_append.argtypes = [CP, P, U64, P, U64, P, U64, P]
+    lib.wc_fp4_cache_read.argtypes = [CP, P, U64, P, P, P]
+    lib.wc_fp4_attention_workspace_bytes.argtypes = [CP, AP]
+    lib.wc_fp4_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.wc_fp4_attention.argtypes = [CP, AP, P, P, P, P, P, P, ctypes.c_size_t, P]
+    for f in (lib.wc_fp4_cache_append, lib.wc_fp4_cache_read, lib.wc_fp4_attention, lib.wc_fp4_encode, lib.wc_fp4_decode, lib.wc_fp4_gemv, lib.wc_moe,
               lib.wc_build_dict, lib.wc_encode, lib.wc_encode_noalloc, lib.wc_decode, lib.wc_decode_gemv,
               lib.wc_gemv_bf16, lib.wc_bits_per_weight, lib.wc_container_crcs,
               lib.wc_artifact_write, lib.wc_artifact_count, lib.wc_artifact_entry,
@@ -672,3 +694,185 @@ def moe(x: torch.Tensor, router: torch.Tensor, gate_up, down, top_k: int, *, sco
                        ctypes.byref(cdn), _ptr(out), _ptr(ids), _ptr(weights), _ptr(work),
                        work.numel(), _stream(stream)), "wc_moe")
     return out, ids, weights
+
+
+# ---- 4-bit cache of keys and values, and attention (include/wc_attn.h) -------
+
+ATTN_MAX_DIM = 256
+ATTN_MAX_NEW = 16
+CACHE_TILE = 32  # tokens; a page is a multiple of it
+
+
+def fp4_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda") -> torch.Tensor:
+    """An empty 4-bit cache: uint8 [pages, kv_heads, page_size / 32, 34 * head_dim],
+    4.25 bits for each number of a key or a value.  head_dim is a multiple of 32
+    up to 256, page_size one of 32."""
+    if page_size % CACHE_TILE or page_size < CACHE_TILE:
+        raise ValueError(f"page_size {page_size} is not a multiple of {CACHE_TILE}")
+    if head_dim % 32 or not 32 <= head_dim <= ATTN_MAX_DIM:
+        raise ValueError(f"head_dim {head_dim} is not a multiple of 32 up to {ATTN_MAX_DIM}")
+    return torch.zeros((pages, kv_heads, page_size // CACHE_TILE, 34 * head_dim), dtype=torch.uint8, device=device)
+
+
+def _cache(cache: torch.Tensor):
+    """(wc_fp4_cache, kv_heads, head_dim) of a checked cache."""
+    if not _on_device(cache):
+        raise ValueError("cache must be a device tensor")
+    if cache.dtype != torch.uint8:
+        raise TypeError("cache must be a uint8 tensor")
+    shape = cache.shape
+    if len(shape) != 4 or shape[3] % (34 * 32) or not 0 < shape[3] <= 34 * ATTN_MAX_DIM or not cache.is_contiguous():
+        raise ValueError(f"cache must be a contiguous [pages, kv_heads, page_size / 32, 34 * head_dim], got "
+                         f"{tuple(shape)}")
+    pages, heads, tiles, width = shape
+    if (heads | tiles * CACHE_TILE) >> 32:
+        raise ValueError(f"cache has shape {tuple(shape)}: a size does not fit 32 bits")
+    return CacheStruct(_ptr(cache), pages, tiles * CACHE_TILE, heads, width // 34), heads, width // 34
+
+
+def _token_rows(t: torch.Tensor, what: str, heads: int | None, dim: int):
+    """(tokens, heads, stride) of BF16 [.., heads, dim] whose leading dimensions
+    are tokens one `stride` of numbers apart: whole tensors, or slices by heads of
+    wider ones."""
+    if not _on_device(t):
+        raise ValueError(f"{what} must be a device tensor")
+    if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+        raise TypeError(f"{what} must hold BF16 bit patterns (bfloat16, int16 or uint16)")
+    shape, strides = t.shape, t.stride()
+    if len(shape) < 3 or shape[-1] != dim or shape[-2] < 1 or (heads is not None and shape[-2] != heads):
+        raise ValueError(f"{what} has shape {tuple(shape)}, expected [.., {'heads' if heads is None else heads}, {dim}]")
+    heads = shape[-2]
+    tokens = shape[:-2].numel()
+    stride, step = heads * dim, 0
+    for n, s in zip(reversed(shape[:-2]), reversed(strides[:-2])):  # from the last to the first
+        if n > 1 and tokens:
+            if not step:
+                stride = step = s
+            elif s != step:
+                raise ValueError(f"{what}: tokens of strides {strides} are not one step apart")
+        step *= n
+    if tokens and (strides[-1] != 1 or (heads > 1 and strides[-2] != dim) or stride < heads * dim or stride % 8):
+        raise ValueError(f"{what}: strides {strides}; a token's heads must be contiguous and tokens a multiple of 8 "
+                         f"numbers apart")
+    return tokens, heads, stride
+
+
+def _whole(t: torch.Tensor, what: str, dtype, shape) -> torch.Tensor:
+    """A contiguous device tensor of that type and shape."""
+    if not _on_device(t):
+        raise ValueError(f"{what} must be a device tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def fp4_cache_append(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None):
+    """wc_fp4_cache_append: keys and values [tokens, kv_heads, head_dim] BF16 into
+    the slots (int64 [tokens]: page * page_size + place) of the cache, each group of
+    32 numbers with a scale as by fp4_encode.  A token whose slot is outside the
+    cache (-1) is left out; slots of one call must differ.  k and v may be slices
+    by heads of a wider tensor."""
+    c, heads, dim = _cache(cache)
+    tokens, _, ks = _token_rows(k, "k", heads, dim)
+    vt, _, vs = _token_rows(v, "v", heads, dim)
+    if vt != tokens:
+        raise ValueError(f"k holds {tokens} tokens, v {vt}")
+    _whole(slots, "slots", torch.int64, (tokens,))
+    _placed("fp4_cache_append", stream, cache, k, v, slots)
+    _check(_lib.wc_fp4_cache_append(ctypes.byref(c), _ptr(k), ks, _ptr(v), vs, _ptr(slots), tokens,
+                                    _stream(stream)), "wc_fp4_cache_append")
+    return cache
+
+
+def fp4_cache_read(cache: torch.Tensor, slots: torch.Tensor, out=None, stream=None):
+    """wc_fp4_cache_read: (k, v), the BF16 values [tokens, kv_heads, head_dim] that
+    the cache holds for the slots; NaN for a slot outside it."""
+    c, heads, dim = _cache(cache)
+    if slots.dim() != 1:
+        raise ValueError(f"slots must be [tokens], got {tuple(slots.shape)}")
+    _whole(slots, "slots", torch.int64, slots.shape)
+    shape = (slots.shape[0], heads, dim)
+    if out is None:
+        out = tuple(_empty(shape, torch.bfloat16, cache.device, stream) for _ in range(2))
+    for t in out:
+        if tuple(_bits16(t, "out").shape) != shape:
+            raise ValueError(f"out has shape {tuple(t.shape)}, expected {shape}")
+    k, v = out
+    _placed("fp4_cache_read", stream, cache, slots, k, v)
+    _check(_lib.wc_fp4_cache_read(ctypes.byref(c), _ptr(slots), shape[0], _ptr(k), _ptr(v), _stream(stream)),
+           "wc_fp4_cache_read")
+    return k, v
+
+
+def _attention_shape(stride, seqs, new, heads, width, window, scale) -> AttentionShape:
+    if (seqs | new | heads | width | window) >> 32:  # ctypes would take it modulo 2^32
+        raise ValueError(f"seqs {seqs}, new tokens {new}, heads {heads}, table width {width}, window {window}: one "
+                         f"is outside 0..2^32 - 1")
+    return AttentionShape(stride, seqs, new, heads, width, window, scale)
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_need(lib, device, pages, page_size, kv_heads, dim, seqs, new, heads, width, window) -> int:
+    return lib.wc_fp4_attention_workspace_bytes(
+        ctypes.byref(CacheStruct(16, pages, page_size, kv_heads, dim)),
+        ctypes.byref(_attention_shape(heads * dim, seqs, new, heads, width, window, 1.0)))
+
+
+def fp4_attention_workspace_bytes(cache: torch.Tensor, seqs: int, new_tokens: int, heads: int, table_width: int,
+                                  window: int = 0) -> int:
+    """wc_fp4_attention_workspace_bytes: device scratch of one fp4_attention call
+    of that shape on the current device (looked up once for each)."""
+    c, _, _ = _cache(cache)
+    return _attention_need(_lib, torch._C._cuda_getDevice(), c.pages, c.page_size, c.kv_heads, c.head_dim, seqs,
+                           new_tokens, heads, table_width, window)
+
+
+def fp4_attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor, *,
+                  scale: float | None = None, window: int = 0, work: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None, stream=None):
+    """wc_fp4_attention: (out, lse) of the newest tokens of every sequence over the
+    4-bit cache.  q BF16 [seqs, heads, head_dim], or [seqs, new, heads, head_dim] with
+    up to 16 new tokens each, which are in the cache already; table int32
+    [seqs, width], the pages of each sequence in order; lengths int32 [seqs], tokens
+    of each in the cache.  Query i of a sequence of length n is at position
+    n - new + i and attends to the positions up to its own, the last `window` of them
+    (0: all).  heads is a multiple of the cache's; scale: head_dim ** -0.5.
+
+    out BF16 like q, lse fp32 [.., heads]: the logarithm of the sum of the scores'
+    exponentials.  A query without any position gets 0 and -inf.  work: uint8,
+    fp4_attention_workspace_bytes(..) of it; a call with the same one on another
+    stream must not overlap."""
+    c, kv_heads, dim = _cache(cache)
+    tokens, heads, stride = _token_rows(q, "q", None, dim)
+    if q.dim() not in (3, 4):
+        raise ValueError(f"q must be [seqs, heads, head_dim] or [seqs, new, heads, head_dim], got {tuple(q.shape)}")
+    seqs, new = q.shape[0], (q.shape[1] if q.dim() == 4 else 1)
+    if heads % kv_heads:
+        raise ValueError(f"{heads} heads are no multiple of the cache's {kv_heads}")
+    if not 1 <= new <= ATTN_MAX_NEW:
+        raise ValueError(f"{new} new tokens outside 1..{ATTN_MAX_NEW}")
+    if table.dim() != 2:
+        raise ValueError(f"table must be [seqs, width], got {tuple(table.shape)}")
+    width = table.shape[1]
+    _whole(table, "table", torch.int32, (seqs, width))
+    _whole(lengths, "lengths", torch.int32, (seqs,))
+    need = _attention_need(_lib, q.get_device(), c.pages, c.page_size, kv_heads, dim, seqs, new, heads, width, window)
+    shape = _attention_shape(stride, seqs, new, heads, width, window, dim ** -0.5 if scale is None else scale)
+    if out is None:
+        out = _empty(q.shape, torch.bfloat16, q.device, stream)
+    elif tuple(_bits16(out, "out").shape) != tuple(q.shape):
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
+    lse = _empty(q.shape[:-1], torch.float32, q.device, stream)
+    if need:
+        if work is None:
+            work = _empty(need, torch.uint8, q.device, stream, returned=False)
+        _bytes(work, "work", need)
+        _placed("fp4_attention", stream, q, cache, table, lengths, out, work)
+    else:
+        _placed("fp4_attention", stream, q, cache, table, lengths, out)
+    _check(_lib.wc_fp4_attention(ctypes.byref(c), ctypes.byref(shape), _ptr(q), _ptr(table), _ptr(lengths),
+                                 _ptr(out), _ptr(lse), _ptr(work) if need else None, need, _stream(stream)),
+           "wc_fp4_attention")
+    return out, lse

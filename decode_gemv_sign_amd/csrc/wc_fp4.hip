@@ -6,44 +6,6 @@
 
 namespace wc {
 
-// The biased exponent of a group's scale from the largest |w| (BF16 bits
-// without the sign): the smallest e >= 1 with |w| <= 7 * 2^(e - 127).
-// |w| = 1.m * 2^(E - 127) is within 7 * 2^(E - 2 - 127) exactly when
-// 1.m <= 1.75, that is m <= 0x60.
-__device__ inline uint32_t fp4_exponent(uint32_t top) {
-  const int e = (int)(top >> 7) - 2 + ((top & 0x7Fu) > 0x60u ? 1 : 0);
-  return top >= 0x7F80u ? 255u : (uint32_t)(e < 1 ? 1 : e);
-}
-
-// 8 BF16 values / 2^(e - 127) to the nearest code, ties to even (the
-// instruction's rounding; above 6 it gives 6, and no value is above 7).
-__device__ inline uint32_t fp4_pack8(u32x4 w, uint32_t e) {
-  const float s = fp4_scale(e);
-  // whole dwords first: a bit cast of a vector's element reads element 0
-  const uint32_t w0 = w[0], w1 = w[1], w2 = w[2], w3 = w[3];
-  uint32_t c = 0;
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(mfma_bf16x2, w0), s, 0);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(mfma_bf16x2, w1), s, 1);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(mfma_bf16x2, w2), s, 2);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(mfma_bf16x2, w3), s, 3);
-  if (e == 253u) {  // code 6 (4 * 2^126) is past BF16: it becomes 5
-    const uint32_t six = c >> 2 & c >> 1 & ~c & 0x11111111u;
-    c -= six;
-  }
-  return e == 255u ? 0u : c;
-}
-
-__device__ inline uint32_t max_abs8(u32x4 w) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-    m = m > lo ? m : lo;
-    m = m > hi ? m : hi;
-  }
-  return m;
-}
-
 // A lane codes 8 columns; the four lanes of a group share their maximum.
 // Blocks walk the rows' pieces of 8 columns, 4 G per row.  Bound by HBM:
 // 24576 x 6144 in 66 us, 382 MB at 5.8 TB/s (a plain copy of 2 GiB: 4.9); 73 us with

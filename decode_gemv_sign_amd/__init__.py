@@ -12,9 +12,10 @@ de un LLM?").
 Next to it a 4-bit tier that loses precision, for tensors that 12 bits per
 weight leave too large (fp4_encode, fp4_decode, fp4_gemv; include/wc_fp4.h),
 a mixture-of-experts layer for a few tokens on BF16 or 4-bit experts
-(moe; include/wc_moe.h), and a cache of keys and values in the same 4-bit form
+(moe; include/wc_moe.h), a cache of keys and values in the same 4-bit form
 with the attention over it (fp4_cache, fp4_cache_append, fp4_cache_read,
-fp4_attention; include/wc_attn.h).
+fp4_attention), and the attention of whole prompts (prompt_attention;
+include/wc_attn.h).
 
 This module only marshals arguments: every step runs in the HIP kernels of
 libwc.so, on the caller's current torch stream.  PyTorch provides device
@@ -37,6 +38,7 @@ __all__ = [
     "artifact_verify", "LIB_PATH",
     "Fp4", "fp4_encode", "fp4_decode", "fp4_gemv", "SOFTMAX", "SIGMOID", "moe", "moe_workspace_bytes",
     "fp4_cache", "fp4_cache_append", "fp4_cache_read", "fp4_attention", "fp4_attention_workspace_bytes",
+    "prompt_attention",
 ]
 
 BYTESPLIT = 0
@@ -118,6 +120,13 @@ class AttentionShape(ctypes.Structure):
         ("scale", ctypes.c_float)]
 
 
+class PromptShape(ctypes.Structure):
+    """wc_prompt_shape (include/wc_attn.h)."""
+    _fields_ = [(n, ctypes.c_uint64) for n in ("tokens", "q_stride", "k_stride", "v_stride")] + [
+        (n, ctypes.c_uint32) for n in ("seqs", "heads", "kv_heads", "head_dim", "window")] + [
+        ("scale", ctypes.c_float)]
+
+
 def _load(path: str = LIB_PATH):
     if not os.path.exists(path):
         raise ImportError(
@@ -157,7 +166,8 @@ def _load(path: str = LIB_PATH):
     lib.wc_fp4_attention_workspace_bytes.argtypes = [CP, AP]
     lib.wc_fp4_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.wc_fp4_attention.argtypes = [CP, AP, P, P, P, P, P, P, ctypes.c_size_t, P]
-    for f in (lib.wc_fp4_cache_append, lib.wc_fp4_cache_read, lib.wc_fp4_attention, lib.wc_fp4_encode, lib.wc_fp4_decode, lib.wc_fp4_gemv, lib.wc_moe,
+    lib.wc_prompt_attention.argtypes = [ctypes.POINTER(PromptShape), P, P, P, P, P, P, P]
+    for f in (lib.wc_prompt_attention, lib.wc_fp4_cache_append, lib.wc_fp4_cache_read, lib.wc_fp4_attention, lib.wc_fp4_encode, lib.wc_fp4_decode, lib.wc_fp4_gemv, lib.wc_moe,
               lib.wc_build_dict, lib.wc_encode, lib.wc_encode_noalloc, lib.wc_decode, lib.wc_decode_gemv,
               lib.wc_gemv_bf16, lib.wc_bits_per_weight, lib.wc_container_crcs,
               lib.wc_artifact_write, lib.wc_artifact_count, lib.wc_artifact_entry,
@@ -875,4 +885,48 @@ def fp4_attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, len
     _check(_lib.wc_fp4_attention(ctypes.byref(c), ctypes.byref(shape), _ptr(q), _ptr(table), _ptr(lengths),
                                  _ptr(out), _ptr(lse), _ptr(work) if need else None, need, _stream(stream)),
            "wc_fp4_attention")
+    return out, lse
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor, *,
+                     scale: float | None = None, window: int = 0, out: torch.Tensor | None = None, stream=None):
+    """wc_prompt_attention: (out, lse) of causal attention over whole prompts,
+    packed one after the other.  q BF16 [tokens, heads, head_dim], k and v [tokens,
+    kv_heads, head_dim], each possibly a slice by heads of a wider tensor; starts
+    int32 [seqs + 1], not falling: sequence i is the tokens starts[i] ..
+    starts[i + 1] - 1.  head_dim is a multiple of 32 up to 256, heads one of
+    kv_heads; a token attends to its sequence up to itself, the last `window` tokens
+    of it (0: all); scale: head_dim ** -0.5.
+
+    out BF16 [tokens, heads, head_dim], lse fp32 [tokens, heads]; rows of tokens of no
+    sequence are not written."""
+    dim = q.shape[-1] if q.dim() else 0
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError(f"q, k and v must be [tokens, heads, head_dim], got {tuple(q.shape)}, {tuple(k.shape)} and "
+                         f"{tuple(v.shape)}")
+    if dim % 32 or not 32 <= dim <= ATTN_MAX_DIM:
+        raise ValueError(f"head_dim {dim} is not a multiple of 32 up to {ATTN_MAX_DIM}")
+    tokens, heads, qs = _token_rows(q, "q", None, dim)
+    kt, kv_heads, ks = _token_rows(k, "k", None, dim)
+    vt, _, vs = _token_rows(v, "v", kv_heads, dim)
+    if kt != tokens or vt != tokens:
+        raise ValueError(f"q holds {tokens} tokens, k {kt}, v {vt}")
+    if heads % kv_heads:
+        raise ValueError(f"{heads} heads are no multiple of {kv_heads}")
+    if starts.dim() != 1 or starts.shape[0] < 1:
+        raise ValueError(f"starts must be [seqs + 1], got {tuple(starts.shape)}")
+    seqs = starts.shape[0] - 1
+    _whole(starts, "starts", torch.int32, (seqs + 1,))
+    if window >> 32:
+        raise ValueError(f"window {window} is outside 0..2^32 - 1")
+    shape = (tokens, heads, dim)
+    if out is None:
+        out = _empty(shape, torch.bfloat16, q.device, stream)
+    elif tuple(_bits16(out, "out").shape) != shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
+    lse = _empty(shape[:-1], torch.float32, q.device, stream)
+    _placed("prompt_attention", stream, q, k, v, starts, out)
+    c = PromptShape(tokens, qs, ks, vs, seqs, heads, kv_heads, dim, window, dim ** -0.5 if scale is None else scale)
+    _check(_lib.wc_prompt_attention(ctypes.byref(c), _ptr(q), _ptr(k), _ptr(v), _ptr(starts), _ptr(out), _ptr(lse),
+                                    _stream(stream)), "wc_prompt_attention")
     return out, lse

@@ -359,7 +359,8 @@ __global__ __launch_bounds__(kWave* kAttnWaves) void k_cache_attention(CacheAttn
     if (__ballot(top > m + kSlack)) {
       top = fmaxf(top, __shfl_xor(top, 16, kWave));
       top = fmaxf(top, __shfl_xor(top, 32, kWave));
-      const float now = fmaxf(m, top), to = now == -INFINITY ? 0.0f : now;
+      // queries that need not move keep theirs: no query's bits depend on another's
+      const float now = top > m + kSlack ? top : m, to = now == -INFINITY ? 0.0f : now;
       const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(off - to);
       m = now;
       off = to;

@@ -1,7 +1,7 @@
 /*
  * wc_attn.h — C ABI of libwc, attention of a serving step: a cache of keys and
- * values in the 4-bit form of wc_fp4.h, and attention of a sequence's newest tokens
- * over it.
+ * values in the 4-bit form of wc_fp4.h, attention of a sequence's newest tokens
+ * over it, and attention over whole prompts in BF16.
  *
  * A query at position p of its sequence attends to the positions
  *   max(0, p - window + 1) .. p        (window 0: 0 .. p)
@@ -101,6 +101,27 @@ size_t wc_fp4_attention_workspace_bytes(const wc_fp4_cache *cache, const wc_fp4_
 int wc_fp4_attention(const wc_fp4_cache *cache, const wc_fp4_attention_shape *shape,
                      const uint16_t *d_q, const int32_t *d_table, const int32_t *d_lengths,
                      uint16_t *d_out, float *d_lse, void *d_work, size_t work_bytes, void *stream);
+
+typedef struct wc_prompt_shape {
+  uint64_t tokens;                       /* of all prompts */
+  uint64_t q_stride, k_stride, v_stride; /* elements from one token to the next, below 2^24 */
+  uint32_t seqs;
+  uint32_t heads, kv_heads, head_dim;
+  uint32_t window; /* 0: none */
+  float scale;
+} wc_prompt_shape;
+
+/*
+ * Prompts one after the other: d_q BF16 [tokens][heads][head_dim], d_k and d_v
+ * [tokens][kv_heads][head_dim]; d_starts int32 [seqs + 1], not falling: sequence i
+ * is the tokens d_starts[i] .. d_starts[i + 1] - 1, the first of them at position 0.
+ * (Entries outside 0 .. tokens count as the nearer end.)  d_out BF16
+ * [tokens][heads][head_dim], d_lse fp32 [tokens][heads] or NULL; tokens of no
+ * sequence are left as they were.
+ */
+int wc_prompt_attention(const wc_prompt_shape *shape, const uint16_t *d_q, const uint16_t *d_k,
+                        const uint16_t *d_v, const int32_t *d_starts, uint16_t *d_out, float *d_lse,
+                        void *stream);
 
 #ifdef __cplusplus
 }

@@ -14,8 +14,9 @@ weight leave too large (fp4_encode, fp4_decode, fp4_gemv; include/wc_fp4.h),
 a mixture-of-experts layer for a few tokens on BF16 or 4-bit experts
 (moe; include/wc_moe.h), a cache of keys and values in the same 4-bit form
 with the attention over it (fp4_cache, fp4_cache_append, fp4_cache_read,
-fp4_attention), and the attention of whole prompts (prompt_attention;
-include/wc_attn.h).
+fp4_attention), the attention of whole prompts (prompt_attention;
+include/wc_attn.h), and the log probabilities of tokens (token_logprobs;
+include/wc_logprob.h).
 
 This module only marshals arguments: every step runs in the HIP kernels of
 libwc.so, on the caller's current torch stream.  PyTorch provides device
@@ -38,7 +39,7 @@ __all__ = [
     "artifact_verify", "LIB_PATH",
     "Fp4", "fp4_encode", "fp4_decode", "fp4_gemv", "SOFTMAX", "SIGMOID", "moe", "moe_workspace_bytes",
     "fp4_cache", "fp4_cache_append", "fp4_cache_read", "fp4_attention", "fp4_attention_workspace_bytes",
-    "prompt_attention",
+    "prompt_attention", "token_logprobs", "token_logprobs_workspace_bytes",
 ]
 
 BYTESPLIT = 0
@@ -127,6 +128,11 @@ class PromptShape(ctypes.Structure):
         ("scale", ctypes.c_float)]
 
 
+class LogprobShape(ctypes.Structure):
+    """wc_logprob_shape (include/wc_logprob.h)."""
+    _fields_ = [("stride", ctypes.c_uint64)] + [(n, ctypes.c_uint32) for n in ("rows", "vocab", "kind", "top")]
+
+
 def _load(path: str = LIB_PATH):
     if not os.path.exists(path):
         raise ImportError(
@@ -167,7 +173,11 @@ def _load(path: str = LIB_PATH):
     lib.wc_fp4_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.wc_fp4_attention.argtypes = [CP, AP, P, P, P, P, P, P, ctypes.c_size_t, P]
     lib.wc_prompt_attention.argtypes = [ctypes.POINTER(PromptShape), P, P, P, P, P, P, P]
-    for f in (lib.wc_prompt_attention, lib.wc_fp4_cache_append, lib.wc_fp4_cache_read, lib.wc_fp4_attention, lib.wc_fp4_encode, lib.wc_fp4_decode, lib.wc_fp4_gemv, lib.wc_moe,
+    LP = ctypes.POINTER(LogprobShape)
+    lib.wc_token_logprobs_workspace_bytes.argtypes = [LP]
+    lib.wc_token_logprobs_workspace_bytes.restype = ctypes.c_size_t
+    lib.wc_token_logprobs.argtypes = [LP, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+    for f in (lib.wc_token_logprobs, lib.wc_prompt_attention, lib.wc_fp4_cache_append, lib.wc_fp4_cache_read, lib.wc_fp4_attention, lib.wc_fp4_encode, lib.wc_fp4_decode, lib.wc_fp4_gemv, lib.wc_moe,
               lib.wc_build_dict, lib.wc_encode, lib.wc_encode_noalloc, lib.wc_decode, lib.wc_decode_gemv,
               lib.wc_gemv_bf16, lib.wc_bits_per_weight, lib.wc_container_crcs,
               lib.wc_artifact_write, lib.wc_artifact_count, lib.wc_artifact_entry,
@@ -930,3 +940,65 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: 
     _check(_lib.wc_prompt_attention(ctypes.byref(c), _ptr(q), _ptr(k), _ptr(v), _ptr(starts), _ptr(out), _ptr(lse),
                                     _stream(stream)), "wc_prompt_attention")
     return out, lse
+
+
+# ---- log probabilities of tokens (include/wc_logprob.h) ----------------------
+
+LOGPROB_MAX_TOP = 32
+
+
+@functools.lru_cache(maxsize=1024)
+def _logprob_need(lib, device, rows, vocab, f32, top) -> int:
+    return lib.wc_token_logprobs_workspace_bytes(ctypes.byref(LogprobShape(vocab, rows, vocab, f32, top)))
+
+
+def token_logprobs_workspace_bytes(rows: int, vocab: int, top: int = 0, dtype=torch.float32) -> int:
+    """wc_token_logprobs_workspace_bytes: device scratch of one token_logprobs call
+    of that shape on the current device (looked up once for each)."""
+    return _logprob_need(_lib, torch._C._cuda_getDevice(), rows, vocab, dtype == torch.float32, top)
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, *, work: torch.Tensor | None = None,
+                   stream=None):
+    """wc_token_logprobs: (logprobs [rows], entropy [rows], top_ids [rows, top] int32,
+    top_logprobs [rows, top]) of logits [rows, vocab], fp32 (as fp4_gemv and
+    decode_gemv give them) or BF16, whose rows may be further apart than vocab.
+    tokens int64 [rows]: the log probability of each under its row's softmax; the
+    entropy in nats; the `top` (0..32) most likely tokens, ties to the lower index.
+    Logits of -inf are no alternatives (id -1 and -inf where too few others are
+    left); a token outside the vocabulary gets NaN.  work: uint8,
+    token_logprobs_workspace_bytes(..) of it; a call with the same one on another
+    stream must not overlap."""
+    if not _on_device(logits):
+        raise ValueError("logits must be a device tensor")
+    f32 = logits.dtype == torch.float32
+    if not f32 and logits.dtype != torch.bfloat16:
+        raise TypeError("logits must be float32 or bfloat16")
+    if logits.dim() != 2 or logits.shape[1] < 1:
+        raise ValueError(f"logits must be [rows, vocab], got {tuple(logits.shape)}")
+    rows, vocab = logits.shape
+    if (rows | vocab) >> 31:
+        raise ValueError(f"logits have shape {tuple(logits.shape)}: a size does not fit 31 bits")
+    if not 0 <= top <= LOGPROB_MAX_TOP:
+        raise ValueError(f"top {top} outside 0..{LOGPROB_MAX_TOP}")
+    stride = logits.stride(0) if rows > 1 else vocab
+    if (vocab > 1 and logits.stride(1) != 1) or stride < vocab:
+        raise ValueError(f"logits of strides {logits.stride()}: a row must be contiguous and rows must not overlap")
+    _whole(tokens, "tokens", torch.int64, (rows,))
+    need = _logprob_need(_lib, logits.get_device(), rows, vocab, f32, top)
+    where = logits.device
+    logprobs, entropy = (_empty((rows,), torch.float32, where, stream) for _ in range(2))
+    ids = _empty((rows, top), torch.int32, where, stream)
+    best = _empty((rows, top), torch.float32, where, stream)
+    if need:
+        if work is None:
+            work = _empty(need, torch.uint8, where, stream, returned=False)
+        _bytes(work, "work", need)
+        _placed("token_logprobs", stream, logits, tokens, work)
+    else:
+        _placed("token_logprobs", stream, logits, tokens)
+    c = LogprobShape(stride, rows, vocab, f32, top)
+    _check(_lib.wc_token_logprobs(ctypes.byref(c), _ptr(logits), _ptr(tokens), _ptr(logprobs), _ptr(entropy),
+                                  _ptr(ids), _ptr(best), _ptr(work) if need else None, need, _stream(stream)),
+           "wc_token_logprobs")
+    return logprobs, entropy, ids, best

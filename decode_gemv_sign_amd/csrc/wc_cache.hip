@@ -127,7 +127,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_cache_read(Cache c, const int
 // ---- attention ---------------------------------------------------------------
 //
 // A block takes up to 16 queries (columns) of one sequence that share a head of
-// keys, and a chunk of the sequence's tiles; its waves take the tiles in turn and
+// keys, and a share of the sequence's tiles; its waves take the tiles in turn and
 // join their sums at the end.  Keys times queries: one MFMA has 16 tokens as rows
 // and 32 columns of the head; a lane receives the scores of 4 tokens with its query
 // (column lane % 16).  The tokens are assigned to the rows so that after two of
@@ -157,94 +157,148 @@ struct CacheAttn {
   const int32_t* lengths;
   uint16_t* out;
   float* lse;   // may be null
-  float* part;  // [(seq, kv head, column tile)][split][columns][dim]
-  float2* top;  // [..][split][columns]: m and the sum of weights
-  uint32_t seqs, news, heads, group, width, window;
-  uint32_t col_tiles, splits, chunk;  // chunk: tiles of a split
-  float scale;                        // times log2(e)
+  float* part;  // [head of keys][column tile][share + seqs blocks][columns][dim]
+  float2* top;  // [..][columns]: m and the sum of weights
+  uint32_t seqs, news, heads, group, width;
+  uint32_t window;             // kNoWindow where there is none
+  uint32_t col_tiles, share;   // share: see Shares
+  float scale;                 // times log2(e)
 };
+constexpr uint32_t kNoWindow = 0x7FFFFFC0u;  // past any length
 
-// Which tiles of a sequence are read, and by how many splits.
+// The tiles of a sequence that its queries attend to.  A sequence without any counts
+// as one of them, for the block that writes its empty result.
 struct Span {
-  int32_t len;
-  uint32_t first, end, splits;
+  int32_t len = 0;
+  uint32_t first = 0, end = 0;
+  __device__ __forceinline__ Span() {}
   __device__ __forceinline__ Span(const CacheAttn& a, uint32_t seq) {
     const int32_t n = a.lengths[seq];
     len = n > 0 ? n : 0;
-    const uint32_t cap = a.width * a.c.page_tiles;  // below 2^26 (attn_ok)
+    const uint32_t cap = a.width * a.c.page_tiles;  // at most 2^25 (attn_cut)
     end = ((uint32_t)len + 31u) / 32u;
     end = end < cap ? end : cap;
-    const int64_t lo = a.window ? (int64_t)len - a.news - a.window + 1 : 0;
-    first = lo > 0 ? (uint32_t)(lo / 32) : 0u;
+    const int32_t lo = len - (int32_t)a.news + 1 - (int32_t)a.window;
+    first = lo > 0 ? (uint32_t)lo / 32u : 0u;
     first = first < end ? first : end;
-    splits = (end - first + a.chunk - 1u) / a.chunk;
-    splits = splits ? splits : 1u;
+  }
+  __device__ __forceinline__ uint32_t count() const { return end > first ? end - first : 1u; }
+};
+
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+
+// Inclusive prefix sum across the wave (DPP shifts within rows of 16 lanes, then rows).
+__device__ __forceinline__ uint32_t wave_upto(uint32_t v) {
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+
+// How the blocks of a head are shared out: per = all sequences' tiles / a.share, and a
+// sequence gets the fewest blocks that leave none more than per tiles.  So sequences of
+// any lengths load the card evenly, with at most a.share + a.seqs blocks, and a block
+// has one sequence (blocks that took equal runs of all tiles, with several sequences
+// where they are short, measured 29.6 us where this takes 20.8; 32 sequences up to 8192
+// tokens).  Each wave works this out from the lengths, 64 sequences at a time.
+struct Shares {
+  Span span;              // the lane's sequence, seq0 + lane
+  uint32_t blocks, upto;  // its blocks, and those up to its last
+  uint32_t seq0 = 0, per;
+  __device__ __forceinline__ explicit Shares(const CacheAttn& a) {
+    const uint32_t lane = (uint32_t)lane_id();
+    span = lane < a.seqs ? Span(a, lane) : Span();
+    uint32_t total = wave_total(lane < a.seqs ? span.count() : 0u);
+    for (uint32_t s = kWave; s < a.seqs; s += kWave)
+      total += wave_total(s + lane < a.seqs ? Span(a, s + lane).count() : 0u);
+    per = ((total + a.share - 1u) / a.share + kAttnWaves - 1u) / kAttnWaves * kAttnWaves;
+    count(a, 0);
+  }
+  __device__ __forceinline__ void count(const CacheAttn& a, uint32_t base) {
+    blocks = seq0 + (uint32_t)lane_id() < a.seqs ? (span.count() + per - 1u) / per : 0u;
+    upto = base + wave_upto(blocks);
+  }
+  __device__ __forceinline__ bool next(const CacheAttn& a) {
+    const uint32_t base = lane_value(upto, kWave - 1);
+    seq0 += kWave;
+    if (seq0 >= a.seqs) return false;
+    span = seq0 + (uint32_t)lane_id() < a.seqs ? Span(a, seq0 + (uint32_t)lane_id()) : Span();
+    count(a, base);
+    return true;
+  }
+  // The lane with the sequence of block b; -1: there is no such block.  Wave-uniform.
+  __device__ __forceinline__ int owner(const CacheAttn& a, uint32_t b) {
+    do {
+      const uint64_t hit = __ballot(b < upto);
+      if (hit) return __ffsll((unsigned long long)hit) - 1;
+    } while (next(a));
+    return -1;
+  }
+  __device__ __forceinline__ int find(const CacheAttn& a, uint32_t seq) {
+    while (seq >= seq0 + kWave) next(a);
+    return (int)(seq - seq0);
   }
 };
 
-template <int G>
-struct TileRegs {
-  uint32_t k[2][G];
-  uint32_t ks[(2 * G + 3) / 4];
-  uint32_t v[G][2];
-  uint32_t vs[G][2];
+// N dwords at byte `off` (4 N bytes aligned for N = 1, 2, 4).
+template <int N>
+__device__ __forceinline__ void load_dwords(buffer b, uint32_t off, uint32_t* to) {
+  if constexpr (N >= 4) {
+    const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, 0));
+    each<4>([&](auto i) __attribute__((always_inline)) { to[i] = x[+i]; });
+    load_dwords<N - 4>(b, off + 16u, to + 4);
+  } else if constexpr (N >= 2) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, (int)off, 0, 0));
+    to[0] = x[0];
+    to[1] = x[1];
+    load_dwords<N - 2>(b, off + 8u, to + 2);
+  } else if constexpr (N == 1) {
+    to[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(b, (int)off, 0, 0);
+  }
+}
 
-  __device__ __forceinline__ void load(const uint8_t* t) {
-    const uint32_t lane = (uint32_t)lane_id(), r = lane & 15u, h = lane >> 4;
+// A lane's keys of a tile, and their scales (byte half G + g).
+template <int G>
+struct KeyRegs {
+  uint32_t codes[2][G], scales[(2 * G + 3) / 4];
+  __device__ __forceinline__ void load(buffer b, uint32_t lane) {
+    const uint32_t r = lane & 15u;
     each<2>([&](auto half) __attribute__((always_inline)) {
       each<(G + 3) / 4>([&](auto z) __attribute__((always_inline)) {
         constexpr int w = G - 4 * z < 4 ? G - 4 * z : 4;
-        const uint8_t* p = t + (half * 64u * G + z * 256u + lane * w) * 4u;
-        if constexpr (w == 4) {
-          const u32x4 x = *(const u32x4*)p;
-          each<4>([&](auto i) __attribute__((always_inline)) { k[half][4 * z + i] = x[+i]; });
-        } else if constexpr (w == 2) {
-          const uint2 x = *(const uint2*)p;
-          k[half][4 * z] = x.x;
-          k[half][4 * z + 1] = x.y;
-        } else {
-          each<w>([&](auto i) __attribute__((always_inline)) { k[half][4 * z + i] = ((const uint32_t*)p)[i]; });
-        }
+        load_dwords<w>(b, lane * (w * 4u) + half * 256u * G + z * 1024u, &codes[half][4 * z]);
       });
     });
-    const uint8_t* s = t + 1024u * G + r * 2u * G;
+    const uint32_t off = 1024u * G + r * 2u * G;
     if constexpr (G % 2 == 0) {
-      each<G / 2>([&](auto i) __attribute__((always_inline)) { ks[i] = ((const uint32_t*)s)[i]; });
+      load_dwords<G / 2>(b, off, scales);
     } else {
       each<(2 * G + 3) / 4>([&](auto i) __attribute__((always_inline)) {
-        const uint32_t hi = 2 * i + 1 < G ? ((const uint16_t*)s)[2 * i + 1 < G ? 2 * i + 1 : 0] : 0u;
-        ks[i] = ((const uint16_t*)s)[2 * i] | hi << 16;
+        scales[i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b, (int)(off + 4u * i), 0, 0);
+        if constexpr (2 * i + 1 < G)
+          scales[i] |= (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b, (int)(off + 4u * i + 2u), 0, 0) << 16;
       });
     }
-    each<(G + 1) / 2>([&](auto p) __attribute__((always_inline)) {
-      const uint8_t* from = t + 512u * G + p * 1024u;
-      if constexpr (2 * p + 1 < G) {
-        const u32x4 x = *(const u32x4*)(from + lane * 16u);
-        v[2 * p][0] = x[0];
-        v[2 * p][1] = x[1];
-        v[2 * p + 1][0] = x[2];
-        v[2 * p + 1][1] = x[3];
-      } else {
-        const uint2 x = *(const uint2*)(from + lane * 8u);
-        v[2 * p][0] = x.x;
-        v[2 * p][1] = x.y;
-      }
-    });
-    each<G>([&](auto g) __attribute__((always_inline)) {
-      const uint2 x = *(const uint2*)(t + 1056u * G + h * 8u * G + g * 8u);
-      vs[g][0] = x.x;
-      vs[g][1] = x.y;
-    });
   }
+};
 
-  // Values of the tokens that are not in `keep` (bytes 0xFF or 0) become 0.
-  __device__ __forceinline__ void keep_values(const uint32_t keep[2]) {
-    each<G>([&](auto g) __attribute__((always_inline)) {
-      each<2>([&](auto i) __attribute__((always_inline)) {
-        v[g][i] &= keep[i];
-        vs[g][i] = (vs[g][i] & keep[i]) | (0x7F7F7F7Fu & ~keep[i]);
-      });
+// A lane's values: its pair of columns of each group for 8 tokens, and their scales.
+template <int G>
+struct ValueRegs {
+  uint32_t codes[G][2], scales[G][2];
+  __device__ __forceinline__ void load(buffer b, uint32_t lane) {
+    const uint32_t h = lane >> 4;
+    each<(G + 1) / 2>([&](auto p) __attribute__((always_inline)) {
+      constexpr int w = 2 * p + 1 < G ? 4 : 2;
+      load_dwords<w>(b, 512u * G + p * 1024u + lane * (w * 4u), codes[2 * p]);
     });
+    load_dwords<2 * G>(b, 1056u * G + h * 8u * G, scales[0]);
   }
 };
 
@@ -266,94 +320,117 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, mfma_bf16x2));
 }
 
-// Values of group g for the lane's 8 tokens: the even and the odd column of its pair.
-template <int G>
-__device__ __forceinline__ void value_operands(const TileRegs<G>& t, int g, u32x4& even, u32x4& odd) {
-  uint32_t d[8];
-  each<2>([&](auto i) __attribute__((always_inline)) {
-    each<4>([&](auto b) __attribute__((always_inline)) {
-      d[4 * i + b] = fp4_pair<b>(t.v[g][i], scale_of<b>(t.vs[g][i]));
-    });
-  });
-  each<4>([&](auto j) __attribute__((always_inline)) {
-    even[+j] = __builtin_amdgcn_perm(d[2 * j + 1], d[2 * j], 0x05040100u);
-    odd[+j] = __builtin_amdgcn_perm(d[2 * j + 1], d[2 * j], 0x07060302u);
-  });
+// 0xFF in the bytes of x that are 0xFF, else 0.
+__device__ __forceinline__ uint32_t bytes_ff(uint32_t x) {
+  const uint32_t t = x & ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  return (t >> 7) * 0xFFu;
 }
 
 template <int G, bool DUP>
-__global__ __launch_bounds__(kWave* kAttnWaves) void k_cache_attention(CacheAttn a) {
+__global__ __launch_bounds__(kWave* kAttnWaves, G <= 4 ? 4 : 2) void k_cache_attention(CacheAttn a) {
   constexpr uint32_t D = 32u * G, kCols = DUP ? 8u : 16u;
   __shared__ mfma_f32x4 sums[kAttnWaves][G][2][kWave];
   __shared__ float2 tops[kAttnWaves][16];
-  const uint32_t lane = (uint32_t)lane_id(), wave = (uint32_t)wave_in_block(), h = lane >> 4;
-  uint32_t b = blockIdx.x;
-  const uint32_t kv = b % a.c.heads;
-  b /= a.c.heads;
-  const uint32_t ct = b % a.col_tiles;
-  b /= a.col_tiles;
-  const uint32_t split = b % a.splits, seq = b / a.splits;
-  const Span sp(a, seq);
-  if (split >= sp.splits) return;
-  const uint32_t tile0 = sp.first + split * a.chunk;
-  const uint32_t tile1 = tile0 + a.chunk < sp.end ? tile0 + a.chunk : sp.end;
+  const uint32_t wave = (uint32_t)wave_in_block();
+  const uint32_t kv = blockIdx.x % a.c.heads, rest = blockIdx.x / a.c.heads;
+  const uint32_t ct = rest % a.col_tiles, block = rest / a.col_tiles;
+  const uint32_t lane = (uint32_t)lane_id(), h = lane >> 4;
+  Shares shares(a);
+  const int owner = shares.owner(a, block);
+  if (owner < 0) return;
+  const uint32_t seq = shares.seq0 + (uint32_t)owner, blocks = lane_value(shares.blocks, owner);
+  const uint32_t share = block - (lane_value(shares.upto, owner) - blocks);  // which one of the sequence's
+  const int32_t len = (int32_t)lane_value((uint32_t)shares.span.len, owner);
+  const uint32_t first = lane_value(shares.span.first, owner), end = lane_value(shares.span.end, owner);
+  const uint32_t most_tiles = (end - first + blocks - 1u) / blocks, tile0 = first + share * most_tiles;
+  const uint32_t tiles = tile0 < end ? (end - tile0 < most_tiles ? end - tile0 : most_tiles) : 0u;
 
+  // The pages of 64 tiles, one per lane, and of the next 64; ~0 where there is none.
+  auto pages = [&](uint32_t i) __attribute__((always_inline)) {
+    return i + lane < tiles ? (uint32_t)a.table[(uint64_t)seq * a.width + (tile0 + i + lane) / a.c.page_tiles] : ~0u;
+  };
+  uint32_t page_of = pages(0), ahead = tiles > (uint32_t)kWave ? pages(kWave) : ~0u;
+  uint32_t in_page = (tile0 + wave) % a.c.page_tiles;  // the next tile's place
+  const uint32_t in_step = kAttnWaves % a.c.page_tiles;
   // the lane's query; columns past the last repeat it
   const uint32_t cols = a.news * a.group;
   uint32_t col = ct * kCols + (lane & (kCols - 1u));
   const bool real = col < cols;
   col = real ? col : cols - 1u;
   const uint32_t qi = col / a.group, head = kv * a.group + col - qi * a.group;
-  const int32_t hi = sp.len - (int32_t)a.news + (int32_t)qi;  // its position
-  const int64_t lo = a.window ? (int64_t)hi - a.window + 1 : 0;
+  const int32_t hi = len - (int32_t)a.news + (int32_t)qi;  // its position
   u32x4 q[G];
   {
     const uint16_t* from = a.q + ((uint64_t)seq * a.news + qi) * a.q_stride + (uint64_t)head * D + 8u * h;
     each<G>([&](auto g) __attribute__((always_inline)) { q[g] = *(const u32x4*)(from + 32 * g); });
   }
-  // positions that every query attends to, and that some query does
-  const int64_t all0 = a.window ? (int64_t)sp.len - a.window : 0, all1 = (int64_t)sp.len - a.news;
-  const int64_t any0 = a.window ? (int64_t)sp.len - a.news - a.window + 1 : 0;
 
   float m = -INFINITY, off = 0, sum = 0;  // off: m, or 0 while there is none
+  uint32_t spoilt = 0;                    // groups in which the query attends to a value that is NaN
   mfma_f32x4 acc[G][2];
   each<G>([&](auto g) __attribute__((always_inline)) { acc[g][0] = acc[g][1] = mfma_f32x4{0, 0, 0, 0}; });
 
-  uint32_t pages = 0;  // of the wave's next 64 tiles, one per lane
-  bool bad = false, bad_next = false;
-  auto fetch = [&](uint32_t i, TileRegs<G>& t) __attribute__((always_inline)) {  // the wave's i-th tile
-    if (i % kWave == 0) {
-      const uint32_t mine = tile0 + wave + (i + lane) * kAttnWaves;
-      pages = mine < tile1 ? (uint32_t)a.table[(uint64_t)seq * a.width + mine / a.c.page_tiles] : 0u;
-    }
-    const uint32_t tile = tile0 + wave + i * kAttnWaves;
-    uint32_t page = (uint32_t)__builtin_amdgcn_readlane((int)pages, (int)(i % kWave));
-    bad_next = page >= a.c.pages;
-    page = bad_next ? 0u : page;
-    t.load(a.c.at(page, kv, tile % a.c.page_tiles));
+  // The wave's tiles are wave, wave + kAttnWaves, ..  Past the last one and where there
+  // is no page loads bring 0 and touch no memory.
+  auto next_of = [&](uint32_t i, bool& bad) __attribute__((always_inline)) {
+    const uint32_t page = lane_value(page_of, (int)(i % kWave));
+    bad = page >= a.c.pages;
+    const bool none = bad || i >= tiles;
+    const uint64_t tile = ((uint64_t)(none ? 0u : page) * a.c.heads + kv) * a.c.page_tiles + in_page;
+    in_page += in_step;
+    in_page = in_page >= a.c.page_tiles ? in_page - a.c.page_tiles : in_page;
+    return buffer_of(a.c.data + tile * a.c.tile_bytes(), none ? 0u : a.c.tile_bytes());
   };
-
-  auto step = [&](uint32_t tile, TileRegs<G>& t) __attribute__((always_inline)) {
-    const int64_t p0 = (int64_t)tile * 32;
-    const bool edge = bad || p0 < all0 || p0 + 31 > all1;  // wave-uniform
+  KeyRegs<G> k;
+  ValueRegs<G> v;
+  bool bad = false;
+  if (wave < tiles) {
+    const buffer t = next_of(wave, bad);
+    k.load(t, lane);
+    v.load(t, lane);
+  }
+  for (uint32_t i = wave; i < tiles; i += kAttnWaves) {
+    if ((i + kAttnWaves) / kWave != i / kWave) {
+      page_of = ahead;
+      ahead = pages((i / kWave + 2u) * kWave);
+    }
+    const int32_t p0 = (int32_t)((tile0 + i) * 32u);
+    bool next_bad;
+    const buffer next = next_of(i + kAttnWaves, next_bad);
+    // some query does not attend to some token (wave-uniform)
+    const bool edge = bad || p0 + 31 > len - (int32_t)a.news || p0 <= len - 1 - (int32_t)a.window;
     float s[8];
     each<2>([&](auto half) __attribute__((always_inline)) {
       mfma_f32x4 x = {0, 0, 0, 0};
       each<G>([&](auto g) __attribute__((always_inline)) {
         constexpr int at = half * G + g;
-        x = mfma16(fp4_expand(t.k[half][g], scale_of<at % 4>(t.ks[at / 4])), q[g], x);
+        x = mfma16(fp4_expand(k.codes[half][g], scale_of<at % 4>(k.scales[at / 4])), q[g], x);
       });
-      each<4>([&](auto i) __attribute__((always_inline)) { s[4 * half + i] = x[+i] * a.scale; });
+      each<4>([&](auto j) __attribute__((always_inline)) { s[4 * half + j] = x[+j] * a.scale; });
     });
+    __builtin_amdgcn_sched_barrier(0);
+    k.load(next, lane);
     if (edge) {
-      uint32_t keep[2] = {0, 0};
-      each<8>([&](auto i) __attribute__((always_inline)) {
-        const int64_t p = p0 + 8u * h + i;
-        s[i] = bad ? NAN : s[i];
-        s[i] = p <= hi && p >= lo ? s[i] : -INFINITY;
-        keep[i / 4] |= !bad && p < sp.len && p >= any0 ? 0xFFu << (8 * (i % 4)) : 0u;
+      uint32_t mine[2] = {0, 0}, any[2] = {0, 0};  // tokens that this query, that some query attends to
+      each<8>([&](auto j) __attribute__((always_inline)) {
+        const int32_t p = p0 + (int32_t)(8u * h) + j;
+        const bool ok = (uint32_t)(hi - p) < a.window;
+        s[j] = bad ? NAN : s[j];
+        s[j] = ok ? s[j] : -INFINITY;
+        mine[j / 4] |= ok ? 0xFFu << (8 * (j % 4)) : 0u;
+        any[j / 4] |= (uint32_t)(len - 1 - p) < a.window + a.news - 1u ? 0xFFu << (8 * (j % 4)) : 0u;
       });
-      t.keep_values(keep);
+      // What no query attends to may hold anything and becomes 0.  A NaN scale stands
+      // for 32 NaN values: they become 0 too, and the group is NaN at the end for the
+      // queries that attend to it.
+      each<G>([&](auto g) __attribute__((always_inline)) {
+        each<2>([&](auto j) __attribute__((always_inline)) {
+          const uint32_t nan = bytes_ff(v.scales[g][j]);
+          spoilt |= nan & mine[j] ? 1u << g : 0u;
+          v.codes[g][j] &= any[j] & ~nan;
+          v.scales[g][j] &= any[j] & ~nan;
+        });
+      });
     }
     float top = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
     if (__ballot(top > m + kSlack)) {
@@ -370,9 +447,9 @@ __global__ __launch_bounds__(kWave* kAttnWaves) void k_cache_attention(CacheAttn
         acc[g][1] *= f;
       });
     }
-    each<8>([&](auto i) __attribute__((always_inline)) {
-      s[i] = __builtin_amdgcn_exp2f(s[i] - off);
-      sum += s[i];
+    each<8>([&](auto j) __attribute__((always_inline)) {
+      s[j] = __builtin_amdgcn_exp2f(s[j] - off);
+      sum += s[j];
     });
     u32x4 high, low;
     each<4>([&](auto j) __attribute__((always_inline)) {
@@ -381,68 +458,41 @@ __global__ __launch_bounds__(kWave* kAttnWaves) void k_cache_attention(CacheAttn
       low[+j] = bf16_pair(s[2 * j] - __uint_as_float(x << 16), s[2 * j + 1] - __uint_as_float(x & 0xFFFF0000u));
     });
     if constexpr (DUP) high = lane & 8u ? low : high;
-    auto product = [&](const TileRegs<G>& from, bool take) __attribute__((always_inline)) {
-      each<G>([&](auto g) __attribute__((always_inline)) {
-        u32x4 even, odd;
-        value_operands<G>(from, g, even, odd);
-        mfma_f32x4 x = mfma16(even, high, acc[g][0]), y = mfma16(odd, high, acc[g][1]);
-        if constexpr (!DUP) {
-          x = mfma16(even, low, x);
-          y = mfma16(odd, low, y);
-        }
-        each<4>([&](auto i) __attribute__((always_inline)) {
-          acc[g][0][+i] = take ? x[+i] : acc[g][0][+i];
-          acc[g][1][+i] = take ? y[+i] : acc[g][1][+i];
+    each<G>([&](auto g) __attribute__((always_inline)) {
+      uint32_t d[8];
+      each<2>([&](auto j) __attribute__((always_inline)) {
+        each<4>([&](auto n) __attribute__((always_inline)) {
+          d[4 * j + n] = fp4_pair<n>(v.codes[g][j], scale_of<n>(v.scales[g][j]));
         });
       });
-    };
-    if (edge && a.news > 1) {
-      // a value that is not finite must not reach the queries that do not attend to it
-      bool odd_one = false;
-      each<G>([&](auto g) __attribute__((always_inline)) {
-        each<2>([&](auto i) __attribute__((always_inline)) {
-          each<4>([&](auto b) __attribute__((always_inline)) {
-            odd_one = odd_one || (t.vs[g][i] >> (8 * b) & 0xFFu) >= 253u;
-          });
-        });
+      u32x4 even, odd;  // columns of the lane's pair
+      each<4>([&](auto j) __attribute__((always_inline)) {
+        even[+j] = __builtin_amdgcn_perm(d[2 * j + 1], d[2 * j], 0x05040100u);
+        odd[+j] = __builtin_amdgcn_perm(d[2 * j + 1], d[2 * j], 0x07060302u);
       });
-      if (__ballot(odd_one)) {
-        for (uint32_t j = 0; j < a.news; ++j) {  // each query by itself
-          const int64_t at = (int64_t)sp.len - a.news + j, from = a.window ? at - a.window + 1 : 0;
-          uint32_t keep[2] = {0, 0};
-          each<8>([&](auto i) __attribute__((always_inline)) {
-            const int64_t p = p0 + 8u * h + i;
-            keep[i / 4] |= p <= at && p >= from ? 0xFFu << (8 * (i % 4)) : 0u;
-          });
-          TileRegs<G> mine = t;
-          mine.keep_values(keep);
-          product(mine, qi == j);
-        }
-        return;
+      acc[g][0] = mfma16(even, high, acc[g][0]);
+      acc[g][1] = mfma16(odd, high, acc[g][1]);
+      if constexpr (!DUP) {
+        acc[g][0] = mfma16(even, low, acc[g][0]);
+        acc[g][1] = mfma16(odd, low, acc[g][1]);
       }
-    }
-    product(t, true);
-  };
-
-  const uint32_t mine = tile0 + wave < tile1 ? (tile1 - tile0 - wave + kAttnWaves - 1u) / kAttnWaves : 0u;
-  if (mine) {
-    TileRegs<G> now;
-    fetch(0, now);
-    for (uint32_t i = 0; i + 1u < mine; ++i) {
-      TileRegs<G> next;
-      bad = bad_next;
-      fetch(i + 1u, next);
-      step(tile0 + wave + i * kAttnWaves, now);
-      now = next;
-    }
-    bad = bad_next;
-    step(tile0 + wave + (mine - 1u) * kAttnWaves, now);
+    });
+    __builtin_amdgcn_sched_barrier(0);
+    v.load(next, lane);
+    bad = next_bad;
   }
   // a query at a position past the table attends to itself, which is not there
-  if (hi >= 0 && (uint64_t)hi >= (uint64_t)a.width * a.c.page_tiles * 32u) sum = NAN;
+  if (hi >= 0 && (uint32_t)hi / 32u >= a.width * a.c.page_tiles) sum = NAN;
 
   sum += __shfl_xor(sum, 16, kWave);
   sum += __shfl_xor(sum, 32, kWave);
+  if (__ballot(spoilt)) {
+    spoilt |= (uint32_t)__shfl_xor((int)spoilt, 16, kWave);
+    spoilt |= (uint32_t)__shfl_xor((int)spoilt, 32, kWave);
+    each<G>([&](auto g) __attribute__((always_inline)) {
+      if (spoilt >> g & 1u) acc[g][0] = acc[g][1] = mfma_f32x4{NAN, NAN, NAN, NAN};
+    });
+  }
   each<G>([&](auto g) __attribute__((always_inline)) {
     // the lane's columns of the group in order: 8 h .. 8 h + 7
     sums[wave][g][0][lane] = mfma_f32x4{acc[g][0][0], acc[g][1][0], acc[g][0][1], acc[g][1][1]};
@@ -455,15 +505,12 @@ __global__ __launch_bounds__(kWave* kAttnWaves) void k_cache_attention(CacheAttn
   each<kAttnWaves>([&](auto i) __attribute__((always_inline)) {
     const float2 t = tops[i][lane & 15u];
     w[i] = t.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(t.x - most);
-    // a NaN sum counts although its wave has no largest score
-    total += t.x == -INFINITY ? (t.y != t.y ? t.y : 0.0f) : w[i] * t.y;
+    total += t.x == -INFINITY ? t.y : w[i] * t.y;  // a NaN sum counts although its wave has no largest score
   });
-  const bool whole = sp.splits == 1u;
   const float by = total == 0.0f ? 0.0f : 1.0f / total;
   const bool stores = real && (!DUP || !(lane & 8u));
   const uint64_t row = ((uint64_t)seq * a.news + qi) * a.heads + head;
-  const uint64_t at = ((((uint64_t)seq * a.c.heads + kv) * a.col_tiles + ct) * a.splits + split) * kCols +
-                      (lane & (kCols - 1u));
+  const uint64_t at = (((uint64_t)kv * a.col_tiles + ct) * (a.share + a.seqs) + block) * kCols + (lane & (kCols - 1u));
   for (uint32_t g = wave; g < (uint32_t)G; g += kAttnWaves) {
     mfma_f32x4 x[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
     each<kAttnWaves>([&](auto i) __attribute__((always_inline)) {
@@ -474,7 +521,7 @@ __global__ __launch_bounds__(kWave* kAttnWaves) void k_cache_attention(CacheAttn
       });
     });
     if (!stores) continue;
-    if (whole) {
+    if (blocks == 1u) {
       u32x4 o;
       each<4>([&](auto j) __attribute__((always_inline)) {
         o[+j] = bf16_pair(x[j / 2][2 * (j % 2)] * by, x[j / 2][2 * (j % 2) + 1] * by);
@@ -487,48 +534,78 @@ __global__ __launch_bounds__(kWave* kAttnWaves) void k_cache_attention(CacheAttn
     }
   }
   if (wave == 0 && h == 0 && stores) {
-    if (!whole)
+    if (blocks != 1u)
       a.top[at] = make_float2(most, total);
     else if (a.lse)
       a.lse[row] = total == 0.0f ? -INFINITY : (most == -INFINITY ? total : (most + __builtin_amdgcn_logf(total)) * kLn2);
   }
 }
 
-// The splits of each query, joined: a wave takes one, a lane D / 64 columns or fewer.
+// The shares of a query's sequence, joined by a block: D / 4 lanes take a share's sums,
+// four shares' loads go out together.
 template <int G>
 __global__ __launch_bounds__(kBlockThreads) void k_cache_join(CacheAttn a, uint32_t cols_of_tile) {
-  constexpr uint32_t D = 32u * G;
-  const uint32_t lane = (uint32_t)lane_id();
-  const uint64_t row = (uint64_t)blockIdx.x * (kBlockThreads / kWave) + (uint32_t)wave_in_block();
-  if (row >= (uint64_t)a.seqs * a.news * a.heads) return;
-  const uint32_t head = (uint32_t)(row % a.heads);
-  const uint64_t token = row / a.heads;
-  const uint32_t seq = (uint32_t)(token / a.news), qi = (uint32_t)(token - (uint64_t)seq * a.news);
-  const Span sp(a, seq);
-  if (sp.splits == 1u) return;
+  constexpr uint32_t D = 32u * G, kLanes = D / 4u, kSets = kBlockThreads / kLanes, kWaves = kBlockThreads / kWave;
+  __shared__ float2 both[kWaves];
+  __shared__ mfma_f32x4 sums[kSets][kLanes];
+  const uint32_t lane = (uint32_t)lane_id(), wave = (uint32_t)wave_in_block();
+  const uint64_t row = blockIdx.x;
+  const uint32_t head = (uint32_t)(row % a.heads), token = (uint32_t)(row / a.heads);
+  const uint32_t seq = token / a.news, qi = token - seq * a.news;
+  Shares shares(a);
+  const int owner = shares.find(a, seq);
+  const uint32_t n = lane_value(shares.blocks, owner), block0 = lane_value(shares.upto, owner) - n;
+  if (n == 1u) return;
   const uint32_t kv = head / a.group, col = qi * a.group + head - kv * a.group;
   const uint32_t ct = col / cols_of_tile;
-  const uint64_t at = (((uint64_t)seq * a.c.heads + kv) * a.col_tiles + ct) * a.splits * cols_of_tile +
-                      (col - ct * cols_of_tile);
+  const uint64_t from = (((uint64_t)kv * a.col_tiles + ct) * (a.share + a.seqs) + block0) * cols_of_tile +
+                        (col - ct * cols_of_tile);
+  auto place = [&](uint32_t s) __attribute__((always_inline)) { return from + (uint64_t)s * cols_of_tile; };
   float most = -INFINITY, total = 0;
-  for (uint32_t s = lane; s < sp.splits; s += kWave) most = fmaxf(most, a.top[at + (uint64_t)s * cols_of_tile].x);
+  for (uint32_t s = threadIdx.x; s < n; s += kBlockThreads) most = fmaxf(most, a.top[place(s)].x);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, kWave));
-  float x[(D + 63) / 64] = {};
-  for (uint32_t s = 0; s < sp.splits; ++s) {
-    const float2 t = a.top[at + (uint64_t)s * cols_of_tile];
-    const float w = t.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(t.x - most);
-    total += t.x == -INFINITY ? (t.y != t.y ? t.y : 0.0f) : w * t.y;
-    const float* from = a.part + (at + (uint64_t)s * cols_of_tile) * D;
+  if (lane == 0) both[wave].x = most;
+  __syncthreads();
 #pragma unroll
-    for (uint32_t i = 0; i < (D + 63) / 64; ++i)
-      if (64u * i + lane < D) x[i] += w * from[64u * i + lane];
+  for (uint32_t i = 0; i < kWaves; ++i) most = fmaxf(most, both[i].x);
+  for (uint32_t s = threadIdx.x; s < n; s += kBlockThreads) {
+    const float2 t = a.top[place(s)];
+    total += t.x == -INFINITY ? t.y : __builtin_amdgcn_exp2f(t.x - most) * t.y;  // t.y is 0 or NaN there
   }
-  const float by = total == 0.0f ? 0.0f : 1.0f / total;
+  total = wave_sum_f32(total);
+  if (lane == 0) both[wave].y = total;
+  const uint32_t set = threadIdx.x / kLanes, mine = threadIdx.x - set * kLanes;
+  mfma_f32x4 x = {0, 0, 0, 0};
+  if (set < kSets) {
+    for (uint32_t s0 = set; s0 < n; s0 += 4u * kSets) {
+      float w[4];
+      mfma_f32x4 y[4];
+      each<4>([&](auto i) __attribute__((always_inline)) {
+        const bool in = s0 + kSets * i < n;
+        const uint64_t at = place(in ? s0 + kSets * i : s0);
+        const float t = a.top[at].x;
+        w[i] = in && t != -INFINITY ? __builtin_amdgcn_exp2f(t - most) : 0.0f;
+        y[i] = *(const mfma_f32x4*)(a.part + at * D + 4u * mine);
+      });
+      each<4>([&](auto i) __attribute__((always_inline)) { x += w[i] * y[i]; });
+    }
+    sums[set][mine] = x;
+  }
+  __syncthreads();
+  total = 0;
 #pragma unroll
-  for (uint32_t i = 0; i < (D + 63) / 64; ++i)
-    if (64u * i + lane < D) a.out[row * D + 64u * i + lane] = bf16_of(x[i] * by);
-  if (lane == 0 && a.lse)
+  for (uint32_t i = 0; i < kWaves; ++i) total += both[i].y;
+  if (set == 0) {
+#pragma unroll
+    for (uint32_t i = 1; i < kSets; ++i) x += sums[i][mine];
+    const float by = total == 0.0f ? 0.0f : 1.0f / total;
+    uint2 o;
+    o.x = bf16_pair(x[0] * by, x[1] * by);
+    o.y = bf16_pair(x[2] * by, x[3] * by);
+    *(uint2*)(a.out + row * D + 4u * mine) = o;
+  }
+  if (threadIdx.x == 0 && a.lse)
     a.lse[row] = total == 0.0f ? -INFINITY : (most == -INFINITY ? total : (most + __builtin_amdgcn_logf(total)) * kLn2);
 }
 
@@ -554,48 +631,53 @@ uint32_t part_blocks(uint64_t units) {
   return (uint32_t)(b < most ? b : most);
 }
 
-// How a call is cut: columns of a tile, tiles of columns, tiles of a split.
+// How a call is cut: columns of a tile, tiles of columns, and Shares' share.
 struct Cut {
-  uint32_t cols, col_tiles, chunk, splits;
-  uint64_t blocks() const { return (uint64_t)col_tiles * splits; }  // per sequence and head of keys
+  uint32_t cols, col_tiles, share;
+  uint64_t blocks;  // of a head of keys and a tile of columns
+  bool joined;      // some sequence may have more than one block
 };
+#ifndef WC_ATTN_BLOCKS
+#define WC_ATTN_BLOCKS 4
+#endif
 int attn_cut(const wc_fp4_cache* c, const wc_fp4_attention_shape* s, Cut* cut) {
   if (!s || s->new_tokens < 1u || s->new_tokens > WC_ATTN_MAX_NEW) return WC_E_UNSUPPORTED;
   if (s->heads < 1u || s->heads > WC_ATTN_MAX_HEADS || s->heads % c->kv_heads) return WC_E_ARG;
   const uint64_t cap = (uint64_t)s->table_width * (c->page_size / 32u);
-  if (cap >= (1ull << 26)) return WC_E_SIZE;  // positions below 2^31
+  if (cap > (1ull << 25)) return WC_E_SIZE;  // positions below 2^30
   const uint32_t cols = s->new_tokens * (s->heads / c->kv_heads);
   cut->cols = cols <= 8u ? 8u : 16u;
   cut->col_tiles = (cols + cut->cols - 1u) / cut->cols;
-  uint64_t tiles = cap;
+  uint64_t tiles = cap ? cap : 1u;  // of a sequence, at most
   if (s->window) {
     const uint64_t most = ((uint64_t)s->window + s->new_tokens - 1u + 30u) / 32u + 1u;
-    tiles = most < cap ? most : cap;
+    tiles = most < tiles ? most : tiles;
   }
-  const uint64_t rows = (uint64_t)s->seqs * c->kv_heads * cut->col_tiles;
-  uint64_t chunk = (tiles * rows + 4u * cu_count() - 1u) / (4u * cu_count());
-  chunk = chunk < 4u ? 4u : (chunk > 64u ? 64u : (chunk + 3u) & ~3ull);
-  cut->chunk = (uint32_t)chunk;
-  cut->splits = (uint32_t)((tiles + chunk - 1u) / chunk);
-  if (!cut->splits) cut->splits = 1u;
-  if (rows * cut->splits >= (1ull << 24)) return WC_E_SIZE;  // a grid of fewer than 2^32 threads
+  const uint64_t all = tiles * s->seqs, rows = (uint64_t)c->kv_heads * cut->col_tiles;
+  if (all >= (1ull << 30) || (uint64_t)s->seqs * s->new_tokens * s->heads >= (1ull << 24)) return WC_E_SIZE;
+  uint64_t share = (WC_ATTN_BLOCKS * cu_count() + rows - 1u) / rows;
+  share = share > s->seqs + share / 4u ? share - s->seqs : share / 4u + 1u;  // with seqs blocks more the card is full
+  const uint64_t most = (all + kAttnWaves - 1u) / kAttnWaves;  // a tile for each wave
+  share = share < most ? share : most;
+  cut->share = share ? (uint32_t)share : 1u;
+  cut->blocks = cut->share + s->seqs;
+  // a sequence of at most `per` tiles has one block, and per is at least kAttnWaves
+  cut->joined = tiles > kAttnWaves && cut->share > 1u;
+  if (cut->blocks * rows >= (1ull << 24)) return WC_E_SIZE;  // grids of fewer than 2^32 threads
   return WC_OK;
 }
-uint64_t attn_partials(const wc_fp4_cache* c, const wc_fp4_attention_shape* s, const Cut& cut) {
-  return cut.splits == 1u ? 0u : (uint64_t)s->seqs * c->kv_heads * cut.blocks() * cut.cols;
+uint64_t attn_partials(const wc_fp4_cache* c, const Cut& cut) {
+  return cut.joined ? (uint64_t)c->kv_heads * cut.col_tiles * cut.blocks * cut.cols : 0u;
 }
 
 template <int G>
 void launch_attention(const CacheAttn& a, const Cut& cut, hipStream_t s) {
-  const uint32_t blocks = a.seqs * a.c.heads * cut.col_tiles * cut.splits;
+  const uint32_t blocks = a.c.heads * cut.col_tiles * (uint32_t)cut.blocks;
   if (cut.cols == 8u)
     k_cache_attention<G, true><<<blocks, kWave * kAttnWaves, 0, s>>>(a);
   else
     k_cache_attention<G, false><<<blocks, kWave * kAttnWaves, 0, s>>>(a);
-  if (cut.splits > 1u) {
-    const uint32_t rows = a.seqs * a.news * a.heads;
-    k_cache_join<G><<<(rows + 3u) / 4u, kBlockThreads, 0, s>>>(a, cut.cols);
-  }
+  if (cut.joined) k_cache_join<G><<<a.seqs * a.news * a.heads, kBlockThreads, 0, s>>>(a, cut.cols);
 }
 
 }  // namespace
@@ -633,7 +715,7 @@ extern "C" size_t wc_fp4_attention_workspace_bytes(const wc_fp4_cache* cache,
                                                    const wc_fp4_attention_shape* shape) {
   wc::Cut cut;
   if (wc::cache_ok(cache) || wc::attn_cut(cache, shape, &cut)) return 0;
-  const uint64_t n = wc::attn_partials(cache, shape, cut);
+  const uint64_t n = wc::attn_partials(cache, cut);
   return n * (cache->head_dim + 2u) * 4u;
 }
 
@@ -652,7 +734,7 @@ extern "C" int wc_fp4_attention(const wc_fp4_cache* cache, const wc_fp4_attentio
   if (!d_q || !wc::aligned16(d_q) || !d_out || !wc::aligned16(d_out) || ((uintptr_t)d_lse & 3u)) return WC_E_ARG;
   if (!d_lengths || ((uintptr_t)d_lengths & 3u)) return WC_E_ARG;
   if (shape->table_width && (!d_table || ((uintptr_t)d_table & 3u))) return WC_E_ARG;
-  const uint64_t n = wc::attn_partials(cache, shape, cut);
+  const uint64_t n = wc::attn_partials(cache, cut);
   if (n) {
     if (!d_work || !wc::aligned16(d_work)) return WC_E_ARG;
     if (work_bytes < n * (cache->head_dim + 2u) * 4u) return WC_E_SIZE;
@@ -672,10 +754,9 @@ extern "C" int wc_fp4_attention(const wc_fp4_cache* cache, const wc_fp4_attentio
   a.heads = shape->heads;
   a.group = shape->heads / cache->kv_heads;
   a.width = shape->table_width;
-  a.window = shape->window;
+  a.window = shape->window && shape->window < wc::kNoWindow ? shape->window : wc::kNoWindow;
   a.col_tiles = cut.col_tiles;
-  a.splits = cut.splits;
-  a.chunk = cut.chunk;
+  a.share = cut.share;
   a.scale = shape->scale * wc::kLog2e;
   const hipStream_t s = (hipStream_t)stream;
   switch (a.c.groups) {

@@ -146,6 +146,9 @@ __global__ __launch_bounds__(kBlockThreads) void k_cache_read(Cache c, const int
 // exchange between lanes.  Weights are then up to 2^kSlack, far inside fp32 and
 // BF16.
 constexpr uint32_t kAttnWaves = 4;
+// Of a block that has a whole sequence: as many as its LDS holds the sums of.
+template <int G, bool WHOLE>
+constexpr uint32_t kWavesOf = WHOLE ? (G <= 4 ? 16u : 8u) : kAttnWaves;
 constexpr float kSlack = 16.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -326,22 +329,36 @@ __device__ __forceinline__ uint32_t bytes_ff(uint32_t x) {
   return (t >> 7) * 0xFFu;
 }
 
-template <int G, bool DUP>
-__global__ __launch_bounds__(kWave* kAttnWaves, G <= 4 ? 4 : 2) void k_cache_attention(CacheAttn a) {
-  constexpr uint32_t D = 32u * G, kCols = DUP ? 8u : 16u;
-  __shared__ mfma_f32x4 sums[kAttnWaves][G][2][kWave];
-  __shared__ float2 tops[kAttnWaves][16];
+// WHOLE: a block has a whole sequence, nothing is left to join.
+template <int G, bool DUP, bool WHOLE>
+__global__ __launch_bounds__(kWave * (kWavesOf<G, WHOLE>), G <= 4 ? 4 : 2) void k_cache_attention(CacheAttn a) {
+  constexpr uint32_t D = 32u * G, kCols = DUP ? 8u : 16u, kWaves = (kWavesOf<G, WHOLE>);
+  constexpr uint32_t kHeld = 4u * kCols;  // lanes whose sums are kept
+  __shared__ mfma_f32x4 sums[kWaves][G][2][kHeld];
+  __shared__ float tops[kWaves][16], totals[kWaves][16];
   const uint32_t wave = (uint32_t)wave_in_block();
   const uint32_t kv = blockIdx.x % a.c.heads, rest = blockIdx.x / a.c.heads;
   const uint32_t ct = rest % a.col_tiles, block = rest / a.col_tiles;
   const uint32_t lane = (uint32_t)lane_id(), h = lane >> 4;
-  Shares shares(a);
-  const int owner = shares.owner(a, block);
-  if (owner < 0) return;
-  const uint32_t seq = shares.seq0 + (uint32_t)owner, blocks = lane_value(shares.blocks, owner);
-  const uint32_t share = block - (lane_value(shares.upto, owner) - blocks);  // which one of the sequence's
-  const int32_t len = (int32_t)lane_value((uint32_t)shares.span.len, owner);
-  const uint32_t first = lane_value(shares.span.first, owner), end = lane_value(shares.span.end, owner);
+  uint32_t seq = block, blocks = 1, share = 0;  // share: which one of the sequence's
+  int32_t len;
+  uint32_t first, end;
+  if constexpr (WHOLE) {
+    const Span span(a, seq);
+    len = span.len;
+    first = span.first;
+    end = span.end;
+  } else {
+    Shares shares(a);
+    const int owner = shares.owner(a, block);
+    if (owner < 0) return;
+    seq = shares.seq0 + (uint32_t)owner;
+    blocks = lane_value(shares.blocks, owner);
+    share = block - (lane_value(shares.upto, owner) - blocks);
+    len = (int32_t)lane_value((uint32_t)shares.span.len, owner);
+    first = lane_value(shares.span.first, owner);
+    end = lane_value(shares.span.end, owner);
+  }
   const uint32_t most_tiles = (end - first + blocks - 1u) / blocks, tile0 = first + share * most_tiles;
   const uint32_t tiles = tile0 < end ? (end - tile0 < most_tiles ? end - tile0 : most_tiles) : 0u;
 
@@ -349,14 +366,19 @@ __global__ __launch_bounds__(kWave* kAttnWaves, G <= 4 ? 4 : 2) void k_cache_att
   auto pages = [&](uint32_t i) __attribute__((always_inline)) {
     return i + lane < tiles ? (uint32_t)a.table[(uint64_t)seq * a.width + (tile0 + i + lane) / a.c.page_tiles] : ~0u;
   };
-  uint32_t page_of = pages(0), ahead = tiles > (uint32_t)kWave ? pages(kWave) : ~0u;
+  // (a whole sequence's first pages do not wait for its length)
+  uint32_t page_of = ~0u;
+  if (WHOLE && a.window == kNoWindow)
+    page_of = lane < a.width * a.c.page_tiles ? (uint32_t)a.table[(uint64_t)seq * a.width + lane / a.c.page_tiles] : ~0u;
+  else
+    page_of = pages(0);
+  uint32_t ahead = tiles > (uint32_t)kWave ? pages(kWave) : ~0u;
   uint32_t in_page = (tile0 + wave) % a.c.page_tiles;  // the next tile's place
-  const uint32_t in_step = kAttnWaves % a.c.page_tiles;
+  const uint32_t in_step = kWaves % a.c.page_tiles;
   // the lane's query; columns past the last repeat it
   const uint32_t cols = a.news * a.group;
   uint32_t col = ct * kCols + (lane & (kCols - 1u));
-  const bool real = col < cols;
-  col = real ? col : cols - 1u;
+  col = col < cols ? col : cols - 1u;
   const uint32_t qi = col / a.group, head = kv * a.group + col - qi * a.group;
   const int32_t hi = len - (int32_t)a.news + (int32_t)qi;  // its position
   u32x4 q[G];
@@ -370,7 +392,7 @@ __global__ __launch_bounds__(kWave* kAttnWaves, G <= 4 ? 4 : 2) void k_cache_att
   mfma_f32x4 acc[G][2];
   each<G>([&](auto g) __attribute__((always_inline)) { acc[g][0] = acc[g][1] = mfma_f32x4{0, 0, 0, 0}; });
 
-  // The wave's tiles are wave, wave + kAttnWaves, ..  Past the last one and where there
+  // The wave's tiles are wave, wave + kWaves, ..  Past the last one and where there
   // is no page loads bring 0 and touch no memory.
   auto next_of = [&](uint32_t i, bool& bad) __attribute__((always_inline)) {
     const uint32_t page = lane_value(page_of, (int)(i % kWave));
@@ -389,14 +411,14 @@ __global__ __launch_bounds__(kWave* kAttnWaves, G <= 4 ? 4 : 2) void k_cache_att
     k.load(t, lane);
     v.load(t, lane);
   }
-  for (uint32_t i = wave; i < tiles; i += kAttnWaves) {
-    if ((i + kAttnWaves) / kWave != i / kWave) {
+  for (uint32_t i = wave; i < tiles; i += kWaves) {
+    if ((i + kWaves) / kWave != i / kWave) {
       page_of = ahead;
       ahead = pages((i / kWave + 2u) * kWave);
     }
     const int32_t p0 = (int32_t)((tile0 + i) * 32u);
     bool next_bad;
-    const buffer next = next_of(i + kAttnWaves, next_bad);
+    const buffer next = next_of(i + kWaves, next_bad);
     // some query does not attend to some token (wave-uniform)
     const bool edge = bad || p0 + 31 > len - (int32_t)a.news || p0 <= len - 1 - (int32_t)a.window;
     float s[8];
@@ -493,51 +515,61 @@ __global__ __launch_bounds__(kWave* kAttnWaves, G <= 4 ? 4 : 2) void k_cache_att
       if (spoilt >> g & 1u) acc[g][0] = acc[g][1] = mfma_f32x4{NAN, NAN, NAN, NAN};
     });
   }
-  each<G>([&](auto g) __attribute__((always_inline)) {
-    // the lane's columns of the group in order: 8 h .. 8 h + 7
-    sums[wave][g][0][lane] = mfma_f32x4{acc[g][0][0], acc[g][1][0], acc[g][0][1], acc[g][1][1]};
-    sums[wave][g][1][lane] = mfma_f32x4{acc[g][0][2], acc[g][1][2], acc[g][0][3], acc[g][1][3]};
-  });
-  if (lane < 16u) tops[wave][lane] = make_float2(m, sum);
+  // The waves' sums, on the largest of their offsets, in order.
+  if (lane < 16u) tops[wave][lane] = m;
   __syncthreads();
-  float most = -INFINITY, total = 0, w[kAttnWaves];
-  each<kAttnWaves>([&](auto i) __attribute__((always_inline)) { most = fmaxf(most, tops[i][lane & 15u].x); });
-  each<kAttnWaves>([&](auto i) __attribute__((always_inline)) {
-    const float2 t = tops[i][lane & 15u];
-    w[i] = t.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(t.x - most);
-    total += t.x == -INFINITY ? t.y : w[i] * t.y;  // a NaN sum counts although its wave has no largest score
-  });
-  const float by = total == 0.0f ? 0.0f : 1.0f / total;
-  const bool stores = real && (!DUP || !(lane & 8u));
-  const uint64_t row = ((uint64_t)seq * a.news + qi) * a.heads + head;
-  const uint64_t at = (((uint64_t)kv * a.col_tiles + ct) * (a.share + a.seqs) + block) * kCols + (lane & (kCols - 1u));
-  for (uint32_t g = wave; g < (uint32_t)G; g += kAttnWaves) {
-    mfma_f32x4 x[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-    each<kAttnWaves>([&](auto i) __attribute__((always_inline)) {
-      each<2>([&](auto p) __attribute__((always_inline)) {
-        mfma_f32x4 y = sums[i][g][p][lane];
-        if constexpr (DUP) y += sums[i][g][p][lane ^ 8u];
-        x[p] += w[i] * y;
+  float most = -INFINITY;
+  each<kWaves>([&](auto i) __attribute__((always_inline)) { most = fmaxf(most, tops[i][lane & 15u]); });
+  const float scale = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - most);  // without an offset all is 0 or NaN
+  if (lane < 16u) totals[wave][lane] = sum * scale;
+  const uint32_t held = DUP ? 8u * h + (lane & 7u) : lane;
+  each<G>([&](auto g) __attribute__((always_inline)) {
+    mfma_f32x4 x = acc[g][0] * scale, y = acc[g][1] * scale;
+    if constexpr (DUP) {  // the products with the low parts are 8 lanes further
+      each<4>([&](auto i) __attribute__((always_inline)) {
+        x[+i] += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x[+i]), 0x128, 0xF, 0xF, true));
+        y[+i] += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(y[+i]), 0x128, 0xF, 0xF, true));
       });
-    });
-    if (!stores) continue;
-    if (blocks == 1u) {
-      u32x4 o;
-      each<4>([&](auto j) __attribute__((always_inline)) {
-        o[+j] = bf16_pair(x[j / 2][2 * (j % 2)] * by, x[j / 2][2 * (j % 2) + 1] * by);
-      });
-      *(u32x4*)(a.out + row * D + 32u * g + 8u * h) = o;
-    } else {
-      mfma_f32x4* to = (mfma_f32x4*)(a.part + at * D + 32u * g + 8u * h);
-      to[0] = x[0];
-      to[1] = x[1];
     }
-  }
-  if (wave == 0 && h == 0 && stores) {
-    if (blocks != 1u)
-      a.top[at] = make_float2(most, total);
-    else if (a.lse)
-      a.lse[row] = total == 0.0f ? -INFINITY : (most == -INFINITY ? total : (most + __builtin_amdgcn_logf(total)) * kLn2);
+    // the lane's columns of the group in order: 8 h .. 8 h + 7
+    if (!DUP || !(lane & 8u)) {
+      sums[wave][g][0][held] = mfma_f32x4{x[0], y[0], x[1], y[1]};
+      sums[wave][g][1][held] = mfma_f32x4{x[2], y[2], x[3], y[3]};
+    }
+  });
+  __syncthreads();
+  const uint64_t at = (((uint64_t)kv * a.col_tiles + ct) * (a.share + a.seqs) + block) * kCols;
+  for (uint32_t i = threadIdx.x; i < G * 2u * kHeld; i += kWaves * kWave) {
+    const uint32_t l = i % kHeld, c = l % kCols;
+    // of group i / (2 kHeld), its half p: 4 columns from 32 g + 8 (l / kCols) + 4 p on
+    const uint32_t to = (i / (2u * kHeld)) * 32u + l / kCols * 8u + i / kHeld % 2u * 4u;
+    mfma_f32x4 x = {0, 0, 0, 0};
+    float total = 0;
+    each<kWaves>([&](auto n) __attribute__((always_inline)) {
+      x += (&sums[n][0][0][0])[i];
+      total += totals[n][c];
+    });
+    const uint32_t mine = ct * kCols + c;
+    if (mine >= cols) continue;
+    const uint32_t qj = mine / a.group;
+    const uint64_t row = ((uint64_t)seq * a.news + qj) * a.heads + kv * a.group + mine - qj * a.group;
+    if (blocks == 1u) {
+      const float by = total == 0.0f ? 0.0f : 1.0f / total;
+      uint2 o;
+      o.x = bf16_pair(x[0] * by, x[1] * by);
+      o.y = bf16_pair(x[2] * by, x[3] * by);
+      *(uint2*)(a.out + row * D + to) = o;
+    } else {
+      *(mfma_f32x4*)(a.part + (at + c) * D + to) = x;
+    }
+    if (i < kCols) {
+      float top = -INFINITY;
+      each<kWaves>([&](auto n) __attribute__((always_inline)) { top = fmaxf(top, tops[n][c]); });
+      if (blocks != 1u)
+        a.top[at + c] = make_float2(top, total);
+      else if (a.lse)
+        a.lse[row] = total == 0.0f ? -INFINITY : (top == -INFINITY ? total : (top + __builtin_amdgcn_logf(total)) * kLn2);
+    }
   }
 }
 
@@ -635,11 +667,8 @@ uint32_t part_blocks(uint64_t units) {
 struct Cut {
   uint32_t cols, col_tiles, share;
   uint64_t blocks;  // of a head of keys and a tile of columns
-  bool joined;      // some sequence may have more than one block
+  bool whole;       // a block for each sequence
 };
-#ifndef WC_ATTN_BLOCKS
-#define WC_ATTN_BLOCKS 4
-#endif
 int attn_cut(const wc_fp4_cache* c, const wc_fp4_attention_shape* s, Cut* cut) {
   if (!s || s->new_tokens < 1u || s->new_tokens > WC_ATTN_MAX_NEW) return WC_E_UNSUPPORTED;
   if (s->heads < 1u || s->heads > WC_ATTN_MAX_HEADS || s->heads % c->kv_heads) return WC_E_ARG;
@@ -655,29 +684,42 @@ int attn_cut(const wc_fp4_cache* c, const wc_fp4_attention_shape* s, Cut* cut) {
   }
   const uint64_t all = tiles * s->seqs, rows = (uint64_t)c->kv_heads * cut->col_tiles;
   if (all >= (1ull << 30) || (uint64_t)s->seqs * s->new_tokens * s->heads >= (1ull << 24)) return WC_E_SIZE;
-  uint64_t share = (WC_ATTN_BLOCKS * cu_count() + rows - 1u) / rows;
+  // Whole sequences where a wave has at most four tiles of them and half of the card has
+  // a block (16 sequences of 1000 positions, 16 heads of 64: 9.2 us against 14.4 split
+  // and joined), or where it has one: a block alone draws little from memory (one
+  // sequence of 1500, 8 heads of 128: 12.7 us whole, 9.7 split).
+  const uint64_t waves = c->head_dim <= 128u ? 16u : 8u;
+  cut->whole = tiles <= waves || (tiles <= 4u * waves && rows * s->seqs >= cu_count() / 2u);
+  // four blocks to a compute unit (32 sequences to 8192: 27.2 us; three 28.6, two 32.1, six 29.1)
+  uint64_t share = (4u * cu_count() + rows - 1u) / rows;
   share = share > s->seqs + share / 4u ? share - s->seqs : share / 4u + 1u;  // with seqs blocks more the card is full
   const uint64_t most = (all + kAttnWaves - 1u) / kAttnWaves;  // a tile for each wave
   share = share < most ? share : most;
-  cut->share = share ? (uint32_t)share : 1u;
+  cut->share = cut->whole ? 0u : share ? (uint32_t)share : 1u;
   cut->blocks = cut->share + s->seqs;
-  // a sequence of at most `per` tiles has one block, and per is at least kAttnWaves
-  cut->joined = tiles > kAttnWaves && cut->share > 1u;
-  if (cut->blocks * rows >= (1ull << 24)) return WC_E_SIZE;  // grids of fewer than 2^32 threads
+  if (cut->blocks * rows >= (1ull << 22)) return WC_E_SIZE;  // grids of fewer than 2^32 threads
   return WC_OK;
 }
 uint64_t attn_partials(const wc_fp4_cache* c, const Cut& cut) {
-  return cut.joined ? (uint64_t)c->kv_heads * cut.col_tiles * cut.blocks * cut.cols : 0u;
+  return cut.whole ? 0u : (uint64_t)c->kv_heads * cut.col_tiles * cut.blocks * cut.cols;
 }
 
 template <int G>
 void launch_attention(const CacheAttn& a, const Cut& cut, hipStream_t s) {
   const uint32_t blocks = a.c.heads * cut.col_tiles * (uint32_t)cut.blocks;
+  if (cut.whole) {
+    constexpr uint32_t kThreads = kWave * (kWavesOf<G, true>);
+    if (cut.cols == 8u)
+      k_cache_attention<G, true, true><<<blocks, kThreads, 0, s>>>(a);
+    else
+      k_cache_attention<G, false, true><<<blocks, kThreads, 0, s>>>(a);
+    return;
+  }
   if (cut.cols == 8u)
-    k_cache_attention<G, true><<<blocks, kWave * kAttnWaves, 0, s>>>(a);
+    k_cache_attention<G, true, false><<<blocks, kWave * kAttnWaves, 0, s>>>(a);
   else
-    k_cache_attention<G, false><<<blocks, kWave * kAttnWaves, 0, s>>>(a);
-  if (cut.joined) k_cache_join<G><<<a.seqs * a.news * a.heads, kBlockThreads, 0, s>>>(a, cut.cols);
+    k_cache_attention<G, false, false><<<blocks, kWave * kAttnWaves, 0, s>>>(a);
+  k_cache_join<G><<<a.seqs * a.news * a.heads, kBlockThreads, 0, s>>>(a, cut.cols);
 }
 
 }  // namespace

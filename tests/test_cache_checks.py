@@ -272,7 +272,7 @@ def test_abi_attention():
                        ({"heads": 1026}, -1), ({"q_stride": 248}, -1), ({"q_stride": 260}, -1),
                        ({"q_stride": 1 << 31}, -2), ({"table_width": 1 << 25}, -2), ({"seqs": 1 << 24}, -2)]:
         assert attend(c, shape_struct(**more)) == code, more
-    s = shape_struct()
+    s = shape_struct(table_width=900)
     for more in ({"q": None}, {"q": P + 8}, {"table": None}, {"table": P + 2}, {"lengths": None}, {"lengths": P + 2},
                  {"out": None}, {"out": P + 8}, {"lse": P + 2}, {"work": None}, {"work": P + 8}):
         assert attend(c, s, **more) == -1, more

@@ -38,89 +38,158 @@ __device__ __forceinline__ uint32_t value_scale_place(uint32_t groups, uint32_t 
   return 1056u * groups + ((t >> 3) * groups + g) * 8u + (t & 7u);
 }
 
-// A lane's 8 columns of a token's keys or values.
-struct RowPart {
-  uint64_t token;
-  uint32_t head, group, part;
-  bool values;
-  __device__ __forceinline__ RowPart(uint64_t u, uint32_t per, const Cache& c) {
-    token = u / per;
-    uint32_t r = (uint32_t)(u - token * per);
-    part = r & 3u;
-    r >>= 2;
-    group = r % c.groups;
-    r /= c.groups;
-    values = r >= c.heads;
-    head = values ? r - c.heads : r;
+// Append and read-back take W tokens of one head per block, in two phases joined in
+// LDS: rows (a lane has 8 columns of a token) and places in the tiles.  What a token has
+// in a tile lies scattered, 64 single bytes for 128 columns of values, and a store or
+// load of single bytes takes as long as one of dwords; so four tokens whose slots are
+// an aligned four of a tile are taken together, a dword for each pair of columns.
+// 8192 tokens of 8 heads of 128: 11.6 us to append (42.5 MB, 3.7 TB/s) and 10.0 to read;
+// bytes alone took 24.5 and 15.9.  W is 32, or 4 where that leaves compute units without a
+// block (32 tokens: 3.5 and 3.4 us, of which 2.4 are an empty kernel's; windows of 32 took
+// 4.8 and 4.7).
+constexpr uint32_t kManyTokens = 32, kFewTokens = 4;
+
+template <uint32_t W>
+struct Window {
+  const uint8_t* tile[W];  // null: no such slot
+  uint8_t place[W];        // in the tile
+  bool four[W];            // the token's aligned four is in the window, in order
+
+  // Called by the whole block; a barrier has to follow.
+  __device__ __forceinline__ void open(const Cache& c, const int64_t* slots, uint64_t token0, uint32_t n,
+                                       uint32_t head) {
+    const uint32_t i = threadIdx.x;
+    if (i >= W) return;  // part of the first wave
+    const int64_t slot = i < n ? slots[token0 + i] : -1;
+    const bool in = (uint64_t)slot < (uint64_t)c.pages * c.page_tiles * kTokens;
+    const uint32_t t = in ? (uint32_t)(slot >> 5) : 0u;  // below 2^31 (cache_ok)
+    const uint32_t page = t / c.page_tiles, p = (uint32_t)slot & 3u;
+    tile[i] = in ? c.at(page, head, t - page * c.page_tiles) : nullptr;
+    place[i] = (uint8_t)(slot & 31);
+    // lane i - p holds slot - p, and the three after it follow
+    bool runs = in;
+#pragma unroll
+    for (int o = 1; o < 4; ++o) {
+      const int64_t next = __shfl_down((long long)slot, o, (int)W);
+      runs = runs && i + o < n && next == slot + o;
+    }
+    const uint64_t heads = __ballot(runs && p == 0u);
+    four[i] = in && i >= p && (heads >> (i - p) & 1u);
   }
 };
-__device__ __forceinline__ bool slot_in(const Cache& c, int64_t slot) {
-  return (uint64_t)slot < (uint64_t)c.pages * c.page_tiles * kTokens;
-}
-__device__ __forceinline__ uint8_t* slot_tile(const Cache& c, int64_t slot, uint32_t head) {
-  const uint32_t tile = (uint32_t)(slot >> 5);  // below 2^31 (cache_ok)
-  const uint32_t page = tile / c.page_tiles;
-  return c.at(page, head, tile - page * c.page_tiles);
-}
 
+template <int G, uint32_t W>
 __global__ __launch_bounds__(kBlockThreads) void k_cache_append(Cache c, const uint16_t* __restrict__ k,
                                                                 uint64_t k_stride,
                                                                 const uint16_t* __restrict__ v,
                                                                 uint64_t v_stride,
                                                                 const int64_t* __restrict__ slots,
                                                                 uint64_t tokens) {
-  const uint32_t per = 8u * c.heads * c.groups;
-  const uint64_t total = tokens * per, stride = (uint64_t)gridDim.x * kBlockThreads;
-  // whole quads of lanes share a group, and total is a multiple of 4
-  for (uint64_t u = (uint64_t)blockIdx.x * kBlockThreads + threadIdx.x; u < total; u += stride) {
-    const RowPart r(u, per, c);
-    const uint64_t col = (uint64_t)r.head * c.dim() + 32u * r.group + 8u * r.part;
-    const u32x4 x = *(const u32x4*)((r.values ? v + r.token * v_stride : k + r.token * k_stride) + col);
-    const int64_t slot = slots[r.token];
-    uint32_t m = max_abs8(x);
+  constexpr uint32_t kParts = 4u * G, kUnits = 2u * kParts * W;  // parts of a row: 8 columns each
+  constexpr int kRounds = (kUnits + kBlockThreads - 1) / kBlockThreads;
+  __shared__ Window<W> w;
+  __shared__ uint32_t codes[2][W][kParts];
+  __shared__ uint8_t scales[2][W][G];
+  const uint32_t head = blockIdx.x % c.heads;
+  const uint64_t token0 = (uint64_t)(blockIdx.x / c.heads) * W;
+  const uint32_t n = tokens - token0 < W ? (uint32_t)(tokens - token0) : W;
+  u32x4 x[kRounds];
+  each<kRounds>([&](auto i) __attribute__((always_inline)) {
+    const uint32_t u = (i * kBlockThreads + threadIdx.x) % kUnits;  // whole quads of lanes share a group
+    const uint32_t part = u % kParts, t = u / kParts % W;
+    const uint64_t row = token0 + (t < n ? t : n - 1u);
+    x[i] = *(const u32x4*)((u / (kParts * W) ? v + row * v_stride : k + row * k_stride) + head * 32u * G + 8u * part);
+  });
+  w.open(c, slots, token0, n, head);
+  each<kRounds>([&](auto i) __attribute__((always_inline)) {
+    const uint32_t u = (i * kBlockThreads + threadIdx.x) % kUnits;  // past the last: the same again
+    const uint32_t part = u % kParts, t = u / kParts % W, kind = u / (kParts * W);
+    uint32_t m = max_abs8(x[i]);
     const uint32_t a = (uint32_t)__shfl_xor((int)m, 1, kWave);
     m = m > a ? m : a;
     const uint32_t b = (uint32_t)__shfl_xor((int)m, 2, kWave);
     m = m > b ? m : b;
-    if (!slot_in(c, slot)) continue;  // the same for the quad
-    const uint32_t e = fp4_exponent(m), codes = fp4_pack8(x, e), t = (uint32_t)slot & 31u;
-    uint8_t* const to = slot_tile(c, slot, r.head);
-    if (r.values) {
+    const uint32_t e = fp4_exponent(m);
+    codes[kind][t][part] = fp4_pack8(x[i], e);
+    if (part % 4u == 0) scales[kind][t][part / 4u] = (uint8_t)e;
+  });
+  __syncthreads();
+  // keys: a part of a quad of groups
+  constexpr uint32_t kQuads = (G + 3) / 4;
+  for (uint32_t u = threadIdx.x; u < W * 4u * kQuads; u += kBlockThreads) {
+    const uint32_t p = u % 4u, quad = u / 4u % kQuads * 4u, t = u / (4u * kQuads);
+    if (!w.tile[t]) continue;
+    uint32_t* const to = (uint32_t*)(w.tile[t] + key_place(G, w.place[t], quad, p));
+    if (G % 4 == 0) {
+      *(u32x4*)to = u32x4{codes[0][t][4u * quad + p], codes[0][t][4u * quad + 4u + p],
+                          codes[0][t][4u * quad + 8u + p], codes[0][t][4u * quad + 12u + p]};
+    } else {
+      for (uint32_t i = 0; i < 4u && quad + i < (uint32_t)G; ++i) to[i] = codes[0][t][4u * (quad + i) + p];
+    }
+  }
+  // values: four bytes of a token, or one of four tokens
+  for (uint32_t u = threadIdx.x; u < W * kParts; u += kBlockThreads) {
+    const uint32_t part = u % kParts, g = part / 4u, t = u / kParts;
+    if (!w.tile[t]) continue;
+    uint8_t* const to = (uint8_t*)w.tile[t];
+    if (w.four[t]) {
+      const uint32_t at = w.place[t] & 3u, t0 = t - at;  // this lane: pair 4 (part % 4) + at
+      uint32_t y = 0;
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) y |= (codes[1][t0 + i][part] >> (8u * at) & 0xFFu) << (8u * i);
+      *(uint32_t*)(to + value_place(G, w.place[t0], g, 4u * (part % 4u) + at)) = y;
+    } else {
 #pragma unroll
       for (uint32_t i = 0; i < 4; ++i)
-        to[value_place(c.groups, t, r.group, 4u * r.part + i)] = (uint8_t)(codes >> (8u * i));
-      if (r.part == 0) to[value_scale_place(c.groups, t, r.group)] = (uint8_t)e;
-    } else {
-      *(uint32_t*)(to + key_place(c.groups, t, r.group, r.part)) = codes;
-      if (r.part == 0) to[key_scale_place(c.groups, t, r.group)] = (uint8_t)e;
+        to[value_place(G, w.place[t], g, 4u * (part % 4u) + i)] = (uint8_t)(codes[1][t][part] >> (8u * i));
     }
+  }
+  for (uint32_t u = threadIdx.x; u < W * G * 2u; u += kBlockThreads) {
+    const uint32_t g = u % G, t = u / G % W, kind = u / (G * W);
+    if (!w.tile[t]) continue;
+    uint8_t* const to = (uint8_t*)w.tile[t];
+    to[kind ? value_scale_place(G, w.place[t], g) : key_scale_place(G, w.place[t], g)] = scales[kind][t][g];
   }
 }
 
+template <int G, uint32_t W>
 __global__ __launch_bounds__(kBlockThreads) void k_cache_read(Cache c, const int64_t* __restrict__ slots,
                                                               uint64_t tokens, uint16_t* __restrict__ k,
                                                               uint16_t* __restrict__ v) {
-  const uint32_t per = 8u * c.heads * c.groups;
-  const uint64_t total = tokens * per, stride = (uint64_t)gridDim.x * kBlockThreads;
-  for (uint64_t u = (uint64_t)blockIdx.x * kBlockThreads + threadIdx.x; u < total; u += stride) {
-    const RowPart r(u, per, c);
-    const int64_t slot = slots[r.token];
-    uint32_t codes = 0, e = 255u;  // NaN
-    if (slot_in(c, slot)) {
-      const uint32_t t = (uint32_t)slot & 31u;
-      const uint8_t* const from = slot_tile(c, slot, r.head);
-      if (r.values) {
+  constexpr uint32_t kParts = 4u * G;
+  __shared__ Window<W> w;
+  __shared__ __attribute__((aligned(4))) uint8_t codes[W][kParts * 4u];  // of values
+  const uint32_t head = blockIdx.x % c.heads;
+  const uint64_t token0 = (uint64_t)(blockIdx.x / c.heads) * W;
+  const uint32_t n = tokens - token0 < W ? (uint32_t)(tokens - token0) : W;
+  w.open(c, slots, token0, n, head);
+  __syncthreads();
+  for (uint32_t u = threadIdx.x; u < W * kParts; u += kBlockThreads) {
+    const uint32_t part = u % kParts, g = part / 4u, t = u / kParts;
+    if (!w.tile[t]) continue;
+    if (w.four[t]) {
+      const uint32_t at = w.place[t] & 3u, t0 = t - at;
+      const uint32_t x = *(const uint32_t*)(w.tile[t] + value_place(G, w.place[t0], g, 4u * (part % 4u) + at));
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i)
-          codes |= (uint32_t)from[value_place(c.groups, t, r.group, 4u * r.part + i)] << (8u * i);
-        e = from[value_scale_place(c.groups, t, r.group)];
-      } else {
-        codes = *(const uint32_t*)(from + key_place(c.groups, t, r.group, r.part));
-        e = from[key_scale_place(c.groups, t, r.group)];
-      }
+      for (uint32_t i = 0; i < 4; ++i) codes[t0 + i][4u * part + at] = (uint8_t)(x >> (8u * i));
+    } else {
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i)
+        codes[t][4u * part + i] = w.tile[t][value_place(G, w.place[t], g, 4u * (part % 4u) + i)];
     }
-    const uint64_t at = (r.token * c.heads + r.head) * c.dim() + 32u * r.group + 8u * r.part;
-    *(u32x4*)((r.values ? v : k) + at) = fp4_expand(codes, fp4_scale(e));
+  }
+  __syncthreads();
+  for (uint32_t u = threadIdx.x; u < 2u * kParts * W; u += kBlockThreads) {
+    const uint32_t part = u % kParts, g = part / 4u, t = u / kParts % W, kind = u / (kParts * W);
+    if (t >= n) continue;
+    uint32_t x = 0, e = 255u;  // NaN
+    if (const uint8_t* const from = w.tile[t]) {
+      x = kind ? *(const uint32_t*)&codes[t][4u * part]
+               : *(const uint32_t*)(from + key_place(G, w.place[t], g, part % 4u));
+      e = from[kind ? value_scale_place(G, w.place[t], g) : key_scale_place(G, w.place[t], g)];
+    }
+    const uint64_t at = ((token0 + t) * c.heads + head) * (32u * G) + 8u * part;
+    *(u32x4*)((kind ? v : k) + at) = fp4_expand(x, fp4_scale(e));
   }
 }
 
@@ -658,9 +727,36 @@ Cache cache_of(const wc_fp4_cache* c) {
   return {c->d_data, (uint32_t)c->pages, c->page_size / 32u, c->kv_heads, c->head_dim / 32u};
 }
 
-uint32_t part_blocks(uint64_t units) {
-  const uint64_t b = (units + kBlockThreads - 1) / kBlockThreads, most = (uint64_t)cu_count() * 16u;
-  return (uint32_t)(b < most ? b : most);
+// launch(first token, tokens, blocks, W) for windows of W tokens, a block for each and
+// each head, in launches of fewer than 2^32 threads.
+template <typename F>
+int each_windows(uint64_t tokens, uint32_t heads, F&& launch) {
+  const bool few = tokens / kManyTokens * heads < cu_count();
+  const uint64_t most = (1ull << 23) / heads * kManyTokens;
+  for (uint64_t t = 0; t < tokens; t += most) {
+    const uint64_t n = tokens - t < most ? tokens - t : most;
+    if (few)
+      launch(t, n, (uint32_t)((n + kFewTokens - 1u) / kFewTokens * heads), std::integral_constant<uint32_t, kFewTokens>{});
+    else
+      launch(t, n, (uint32_t)((n + kManyTokens - 1u) / kManyTokens * heads), std::integral_constant<uint32_t, kManyTokens>{});
+    if (const int v = launched()) return v;
+  }
+  return WC_OK;
+}
+
+// f(groups) with the number of groups as a constant.
+template <typename F>
+void by_groups(uint32_t groups, F&& f) {
+  switch (groups) {
+    case 1: f(std::integral_constant<int, 1>{}); break;
+    case 2: f(std::integral_constant<int, 2>{}); break;
+    case 3: f(std::integral_constant<int, 3>{}); break;
+    case 4: f(std::integral_constant<int, 4>{}); break;
+    case 5: f(std::integral_constant<int, 5>{}); break;
+    case 6: f(std::integral_constant<int, 6>{}); break;
+    case 7: f(std::integral_constant<int, 7>{}); break;
+    default: f(std::integral_constant<int, 8>{}); break;
+  }
 }
 
 // How a call is cut: columns of a tile, tiles of columns, and Shares' share.
@@ -735,9 +831,13 @@ extern "C" int wc_fp4_cache_append(const wc_fp4_cache* cache, const uint16_t* d_
   if (tokens == 0) return WC_OK;
   if (!d_k || !wc::aligned16(d_k) || !d_v || !wc::aligned16(d_v) || !d_slots || ((uintptr_t)d_slots & 7u))
     return WC_E_ARG;
-  wc::k_cache_append<<<wc::part_blocks(tokens * row / 4u), wc::kBlockThreads, 0, (hipStream_t)stream>>>(
-      wc::cache_of(cache), d_k, k_stride, d_v, v_stride, d_slots, tokens);
-  return wc::launched();
+  const wc::Cache c = wc::cache_of(cache);
+  return wc::each_windows(tokens, c.heads, [&](uint64_t t, uint64_t n, uint32_t blocks, auto w) {
+    wc::by_groups(c.groups, [&](auto g) {
+      wc::k_cache_append<decltype(g)::value, decltype(w)::value><<<blocks, wc::kBlockThreads, 0, (hipStream_t)stream>>>(
+          c, d_k + t * k_stride, k_stride, d_v + t * v_stride, v_stride, d_slots + t, n);
+    });
+  });
 }
 
 extern "C" int wc_fp4_cache_read(const wc_fp4_cache* cache, const int64_t* d_slots, uint64_t tokens,
@@ -747,10 +847,14 @@ extern "C" int wc_fp4_cache_read(const wc_fp4_cache* cache, const int64_t* d_slo
   if (tokens == 0) return WC_OK;
   if (!d_k || !wc::aligned16(d_k) || !d_v || !wc::aligned16(d_v) || !d_slots || ((uintptr_t)d_slots & 7u))
     return WC_E_ARG;
+  const wc::Cache c = wc::cache_of(cache);
   const uint64_t row = (uint64_t)cache->kv_heads * cache->head_dim;
-  wc::k_cache_read<<<wc::part_blocks(tokens * row / 4u), wc::kBlockThreads, 0, (hipStream_t)stream>>>(
-      wc::cache_of(cache), d_slots, tokens, d_k, d_v);
-  return wc::launched();
+  return wc::each_windows(tokens, c.heads, [&](uint64_t t, uint64_t n, uint32_t blocks, auto w) {
+    wc::by_groups(c.groups, [&](auto g) {
+      wc::k_cache_read<decltype(g)::value, decltype(w)::value><<<blocks, wc::kBlockThreads, 0, (hipStream_t)stream>>>(
+          c, d_slots + t, n, d_k + t * row, d_v + t * row);
+    });
+  });
 }
 
 extern "C" size_t wc_fp4_attention_workspace_bytes(const wc_fp4_cache* cache,
@@ -800,16 +904,6 @@ extern "C" int wc_fp4_attention(const wc_fp4_cache* cache, const wc_fp4_attentio
   a.col_tiles = cut.col_tiles;
   a.share = cut.share;
   a.scale = shape->scale * wc::kLog2e;
-  const hipStream_t s = (hipStream_t)stream;
-  switch (a.c.groups) {
-    case 1: wc::launch_attention<1>(a, cut, s); break;
-    case 2: wc::launch_attention<2>(a, cut, s); break;
-    case 3: wc::launch_attention<3>(a, cut, s); break;
-    case 4: wc::launch_attention<4>(a, cut, s); break;
-    case 5: wc::launch_attention<5>(a, cut, s); break;
-    case 6: wc::launch_attention<6>(a, cut, s); break;
-    case 7: wc::launch_attention<7>(a, cut, s); break;
-    default: wc::launch_attention<8>(a, cut, s); break;
-  }
+  wc::by_groups(a.c.groups, [&](auto g) { wc::launch_attention<decltype(g)::value>(a, cut, (hipStream_t)stream); });
   return wc::launched();
 }

@@ -100,6 +100,41 @@ def test_append_takes_slices_and_leaves_out_slots():
     wc.fp4_cache_append(inside, k[:0], v[:0], slots[:0])
 
 
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("heads,tokens", [(16, 700), (3, 130), (1, 40)])
+def test_append_runs_of_slots(dim, heads, tokens):
+    """Runs of slots of any length from any place on, in order, falling, and with gaps
+    and unused places between: whole aligned fours and parts of them."""
+    rng = np.random.default_rng([dim, heads, tokens])
+    page, pages = 64, 40
+    free = list(rng.permutation(pages))
+    slots = []
+    while len(slots) < tokens:
+        n, at = int(rng.integers(1, 40)), int(rng.integers(0, 25))
+        run = free.pop() * page + at + np.arange(n)
+        kind = rng.integers(0, 5)
+        run = run[::-1] if kind == 0 else run[rng.random(n) < 0.8] if kind == 1 else run
+        slots += run.tolist() + [-1] * int(rng.integers(0, 3) if kind == 2 else 0)
+    slots = np.array(slots[:tokens], dtype=np.int64)
+    k, v = bits(rng, tokens, heads, dim), bits(rng, tokens, heads, dim)
+    cache = wc.fp4_cache(pages, page, heads, dim, DEV)
+    at = torch.from_numpy(slots).to(DEV)
+    wc.fp4_cache_append(cache, dev16(k), dev16(v), at)
+    real = slots >= 0
+    for got, src in zip(wc.fp4_cache_read(cache, at), (k, v)):
+        assert np.array_equal(of(got)[real], attn_ref.held(src)[real])
+        assert np.isnan(of(got)[~real]).all()
+    rest = torch.from_numpy(np.setdiff1d(np.arange(pages * page), slots)).to(DEV)
+    for got in wc.fp4_cache_read(cache, rest):
+        assert bool((got == 0).all())
+    # one by one, the same bytes
+    other = wc.fp4_cache(pages, page, heads, dim, DEV)
+    for part in np.array_split(np.arange(tokens), 7):
+        p = torch.from_numpy(part).to(DEV)
+        wc.fp4_cache_append(other, dev16(k)[p], dev16(v)[p], at[p])
+    assert torch.equal(cache, other)
+
+
 # ---- attention ---------------------------------------------------------------
 
 class Case:

@@ -29,7 +29,8 @@ struct Prompt {
   uint64_t tokens;
   uint32_t q_stride, k_stride, v_stride;
   uint32_t seqs, heads, kv_heads, group, window;
-  float scale;  // times log2(e)
+  float scale;   // times log2(e), not 0
+  float masked;  // a score whose weight is 0: -inf, or +inf where scale is negative
 };
 
 // A block takes 32 queries of one head per wave and walks the tiles of 64 tokens
@@ -43,7 +44,12 @@ struct Prompt {
 // LDS reads that transpose (ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 numbers
 // and receive a column each).  The second product has the head's columns as rows,
 // so that the running maximum and sum of a query stay in its lane pair.
-constexpr float kSlack = 16.0f;  // as in wc_cache.hip: the offset moves when a score passes it by this
+//
+// Weights are exp2(s - offset), the offset a value near the query's largest score so
+// far: it is set at its first tile, and moves (and the tile is done once more) only
+// when the weights of a tile add up to more than kMost.  So a step looks for no
+// maximum, and nothing crosses lanes.
+constexpr float kMost = 65536.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kStepTokens = 64;
 
@@ -62,7 +68,7 @@ struct Place {
 };
 
 template <int G, int NW>
-__global__ __launch_bounds__(kWave* NW) void k_prompt(Prompt a) {
+__global__ __launch_bounds__(kWave* NW, G <= 4 ? 2 : 1) void k_prompt(Prompt a) {
   using P = Place<G>;
   constexpr uint32_t D = 32u * G, kRows = 32u * NW;
   constexpr int kSteps = 2 * G;  // MFMAs over the head's columns
@@ -173,47 +179,73 @@ __global__ __launch_bounds__(kWave* NW) void k_prompt(Prompt a) {
 
   auto step = [&](int32_t tile, uint32_t k) __attribute__((always_inline)) {
     const uint32_t t0 = (uint32_t)tile * kStepTokens, v = k + P::kTile;
-    mfma_f32x16 s[2];
-    each<2>([&](auto t) __attribute__((always_inline)) {
-      each<16>([&](auto i) __attribute__((always_inline)) { s[t][+i] = 0; });
-      each<kSteps>([&](auto i) __attribute__((always_inline)) { s[t] = mfma32(key_operand(k, t, i), q[i], s[t]); });
-    });
     // some query does not attend to some token
     const bool edge = t0 + kStepTokens - 1u > w0 || (a.window && w1 >= a.window && t0 <= w1 - a.window);
-    each<2>([&](auto t) __attribute__((always_inline)) {
-      each<16>([&](auto i) __attribute__((always_inline)) { s[t][+i] *= a.scale; });
-    });
-    if (edge) {
-      int32_t ahead = (int32_t)(pos - t0 - 4u * h);  // of the query, from the lane's first token
-      asm volatile("" : "+v"(ahead));                // what follows is not kept over the tiles
+    mfma_f32x16 s[2];
+    float part;
+    bool need = m == -INFINITY, full = __ballot(need);
+    for (;;) {  // once more where a query's offset has to move
+      // operands a group of four products ahead
+      u32x4 keys[2][4];
+      auto load_keys = [&](auto j) __attribute__((always_inline)) {
+        each<4>([&](auto n) __attribute__((always_inline)) { keys[j % 2][n] = key_operand(k, n % 2, 2 * j + n / 2); });
+      };
+      load_keys(std::integral_constant<int, 0>{});
+      each<2>([&](auto t) __attribute__((always_inline)) {
+        each<16>([&](auto i) __attribute__((always_inline)) { s[t][+i] = 0; });
+      });
+      each<G>([&](auto j) __attribute__((always_inline)) {
+        if constexpr (j + 1 < G) load_keys(std::integral_constant<int, j + 1>{});
+        __builtin_amdgcn_sched_barrier(0);
+        each<4>([&](auto n) __attribute__((always_inline)) { s[n % 2] = mfma32(keys[j % 2][n], q[2 * j + n / 2], s[n % 2]); });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      if (edge) {
+        int32_t ahead = (int32_t)(pos - t0 - 4u * h);  // of the query, from the lane's first token
+        asm volatile("" : "+v"(ahead));                // what follows is not kept over the tiles
+        each<2>([&](auto t) __attribute__((always_inline)) {
+          each<16>([&](auto i) __attribute__((always_inline)) {
+            const int32_t d = ahead - (32 * t + 8 * (i / 4) + i % 4);
+            const bool ok = d >= 0 && (!a.window || (uint32_t)d < a.window);
+            s[t][+i] = ok ? s[t][+i] : a.masked;
+          });
+        });
+      }
+      if (full) {
+        float top = -INFINITY;
+        each<2>([&](auto t) __attribute__((always_inline)) {
+          each<16>([&](auto i) __attribute__((always_inline)) { top = fmaxf(top, s[t][+i] * a.scale); });
+        });
+        top = fmaxf(top, __shfl_xor(top, 32, kWave));
+        // queries that need not move keep theirs: no query's bits depend on another's
+        const float now = need ? top : m, to = now == -INFINITY ? 0.0f : now;
+        const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(off - to);
+        m = now;
+        off = to;
+        sum *= f;
+        each<G>([&](auto g) __attribute__((always_inline)) { acc[g] *= f; });
+      }
+      part = 0;
       each<2>([&](auto t) __attribute__((always_inline)) {
         each<16>([&](auto i) __attribute__((always_inline)) {
-          const int32_t d = ahead - (32 * t + 8 * (i / 4) + i % 4);
-          const bool ok = d >= 0 && (!a.window || (uint32_t)d < a.window);
-          s[t][+i] = ok ? s[t][+i] : -INFINITY;
+          s[t][+i] = __builtin_amdgcn_exp2f(fmaf(s[t][+i], a.scale, -off));
+          part += s[t][+i];
         });
       });
+      if (full) break;
+      need = !(part <= kMost);
+      full = __ballot(need);
+      if (!full) break;
+      const int other = __shfl_xor((int)need, 32, kWave);
+      need = need || other;
     }
-    float top = s[0][0];
+    sum += part;
+    u32x4 values[2][G], w[4];
+    auto load_values = [&](auto c) __attribute__((always_inline)) {
+      each<G>([&](auto g) __attribute__((always_inline)) { values[c % 2][g] = value_operand(v, g, c); });
+    };
+    load_values(std::integral_constant<int, 0>{});
     each<2>([&](auto t) __attribute__((always_inline)) {
-      each<16>([&](auto i) __attribute__((always_inline)) { top = fmaxf(top, s[t][+i]); });
-    });
-    if (__ballot(top > m + kSlack)) {
-      top = fmaxf(top, __shfl_xor(top, 32, kWave));
-      // queries that need not move keep theirs: no query's bits depend on another's
-      const float now = top > m + kSlack ? top : m, to = now == -INFINITY ? 0.0f : now;
-      const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(off - to);
-      m = now;
-      off = to;
-      sum *= f;
-      each<G>([&](auto g) __attribute__((always_inline)) { acc[g] *= f; });
-    }
-    u32x4 w[4];
-    each<2>([&](auto t) __attribute__((always_inline)) {
-      each<16>([&](auto i) __attribute__((always_inline)) {
-        s[t][+i] = __builtin_amdgcn_exp2f(s[t][+i] - off);
-        sum += s[t][+i];
-      });
       each<8>([&](auto i) __attribute__((always_inline)) {
         w[2 * t + i / 4][i % 4] = bf16_pair(s[t][2 * i], s[t][2 * i + 1]);
       });
@@ -234,8 +266,11 @@ __global__ __launch_bounds__(kWave* NW) void k_prompt(Prompt a) {
         return;
       }
     }
-    each<G>([&](auto g) __attribute__((always_inline)) {
-      each<4>([&](auto c) __attribute__((always_inline)) { acc[g] = mfma32(value_operand(v, g, c), w[c], acc[g]); });
+    each<4>([&](auto c) __attribute__((always_inline)) {
+      if constexpr (c + 1 < 4) load_values(std::integral_constant<int, c + 1>{});
+      __builtin_amdgcn_sched_barrier(0);
+      each<G>([&](auto g) __attribute__((always_inline)) { acc[g] = mfma32(values[c % 2][g], w[c], acc[g]); });
+      __builtin_amdgcn_sched_barrier(0);
     });
   };
 
@@ -321,7 +356,7 @@ int launch_prompt(const Prompt& a, const wc_prompt_shape* p, hipStream_t s) {
 template <int G>
 int launch_prompt_of(const Prompt& a, const wc_prompt_shape* p, hipStream_t s) {
   if constexpr (G <= 4)
-    if (prompt_tiles(p, 256) * a.heads >= 2u * cu_count()) return launch_prompt<G, 8>(a, p, s);
+    if (p->tokens / p->seqs >= 4096u && prompt_tiles(p, 256) * a.heads >= 2u * cu_count()) return launch_prompt<G, 8>(a, p, s);
   return launch_prompt<G, 4>(a, p, s);
 }
 
@@ -345,9 +380,11 @@ extern "C" int wc_prompt_attention(const wc_prompt_shape* shape, const uint16_t*
   if (!d_q || !wc::aligned16(d_q) || !d_k || !wc::aligned16(d_k) || !d_v || !wc::aligned16(d_v)) return WC_E_ARG;
   if (!d_starts || ((uintptr_t)d_starts & 3u) || !d_out || !wc::aligned16(d_out) || ((uintptr_t)d_lse & 3u))
     return WC_E_ARG;
+  // a factor that makes every score 0 without making a mask's infinity NaN
+  const float scale = s.scale == 0.0f ? 1e-37f : s.scale * wc::kLog2e;
   const wc::Prompt a = {d_q, d_k, d_v, d_starts, d_out, d_lse, s.tokens, (uint32_t)s.q_stride, (uint32_t)s.k_stride,
                         (uint32_t)s.v_stride, s.seqs, s.heads, s.kv_heads, s.heads / s.kv_heads, s.window,
-                        s.scale * wc::kLog2e};
+                        scale, scale < 0.0f ? INFINITY : -INFINITY};
   const hipStream_t st = (hipStream_t)stream;
   switch (s.head_dim / 32u) {
     case 1: return wc::launch_prompt_of<1>(a, shape, st);

@@ -7,35 +7,36 @@
 namespace wc {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr uint32_t kScoreWaves = 4;
-constexpr int kMine = 16;                         // logits of a lane's batch
-constexpr uint32_t kBatch = kMine * kWave;        // of a wave's
+constexpr int kMine = 16;               // logits of a lane's batch
+constexpr uint32_t kBatch = kMine * kWave;  // of a wave's
+constexpr uint32_t kSingly = 6;  // keys that are put into a list one by one, faster than a merge
+constexpr uint32_t kManyWaves = 4, kFewWaves = 16;  // of a block: see cut_scores
 
-// Running sums of a row: the largest logit m, s = sum exp(x - m) and
-// w = sum (x - m) exp(x - m); lse = m + log s and the entropy log s - w / s, which
-// loses nothing where one token is nearly certain.  m = -inf: nothing but -inf.
+// Running sums of a row: m the largest logit, and with t = (x - m) log2(e), s = sum 2^t
+// and w = sum t 2^t; lse = m + log s and the entropy (log2 s - w / s) ln 2, which loses
+// nothing where one token is nearly certain.  m = -inf: nothing but -inf so far.
 struct Sums3 {
   float m = -INFINITY, s = 0, w = 0;
   // Both over the larger of the two offsets.
   __device__ __forceinline__ void join(float om, float os, float ow) {
     const float top = fmaxf(m, om);
-    // below -200 the factor is 0, which must not meet an infinite distance
-    const float d = m == -INFINITY ? 0.0f : fmaxf(m - top, -200.0f);
-    const float od = om == -INFINITY ? 0.0f : fmaxf(om - top, -200.0f);
-    const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(d * kLog2e);
-    const float of = om == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(od * kLog2e);
+    // below -300 the factor is 0, which must not meet an infinite distance
+    const float d = m == -INFINITY ? 0.0f : fmaxf((m - top) * kLog2e, -300.0f);
+    const float od = om == -INFINITY ? 0.0f : fmaxf((om - top) * kLog2e, -300.0f);
+    const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(d);
+    const float of = om == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(od);
     w = (w + s * d) * f + (ow + os * od) * of;
     s = s * f + os * of;  // a NaN stays one
     m = top;
   }
   __device__ __forceinline__ void add(const float x[kMine], float top) {
-    join(top, 0, 0);
-    const float off = m == -INFINITY ? 0.0f : m;
+    if (__ballot(top > m)) join(top, 0, 0);
+    const float o = m == -INFINITY ? 0.0f : m;
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-      const float u = x[i] - off, e = __builtin_amdgcn_exp2f(u * kLog2e);
+      const float t = (x[i] - o) * kLog2e, e = __builtin_amdgcn_exp2f(t);
       s += e;
-      w = fmaf(fmaxf(u, -200.0f), e, w);  // -inf: 0 times a number
+      w = fmaf(fmaxf(t, -300.0f), e, w);  // -inf: 0 times a number
     }
   }
   __device__ __forceinline__ void join_wave() {
@@ -62,6 +63,22 @@ __device__ __forceinline__ uint64_t lane_key(uint64_t k, int lane) {  // lane: w
          (uint32_t)__builtin_amdgcn_readlane((int)k, lane);
 }
 
+// The wave's values sorted over its lanes, falling (none of them NaN).
+template <typename T>
+__device__ __forceinline__ T wave_sorted(T v) {
+  const uint32_t lane = (uint32_t)lane_id();
+#pragma unroll
+  for (uint32_t k = 2; k <= (uint32_t)kWave; k *= 2) {
+#pragma unroll
+    for (uint32_t j = k / 2; j > 0; j /= 2) {
+      const T other = __shfl_xor(v, (int)j, kWave);
+      const bool larger = !(lane & j) == !(lane & k);  // this lane keeps the larger one
+      v = (v > other) == larger ? v : other;
+    }
+  }
+  return v;
+}
+
 // The largest `top` keys seen, in lanes 0 .. top - 1, falling.
 struct Best {
   uint64_t list = 0, least = 0;  // least: the last one's, 0 while there are fewer
@@ -82,17 +99,18 @@ struct Best {
       least = lane_key(list, (int)top - 1);
     }
   }
-  // A key per lane (0: none) as the first ones: sorted by counting the larger ones.
-  __device__ __forceinline__ void start(uint64_t key, uint64_t* room) {  // room: kWave keys of the wave's own
+  // A key per lane (0: none) at once: both lists falling, one of them turned round, are a
+  // sequence that a merge's last steps sort.
+  __device__ __forceinline__ void merge(uint64_t key) {
     const uint32_t lane = (uint32_t)lane_id();
-    uint32_t rank = 0;
-    for (int i = 0; i < kWave; ++i) rank += lane_key(key, i) > key ? 1u : 0u;
-    room[lane] = 0;
-    wave_lds_sync();
-    if (key) room[rank] = key;
-    wave_lds_sync();
-    list = room[lane];
-    wave_lds_sync();
+    key = (uint64_t)wave_sorted((unsigned long long)key);
+    const uint64_t turned = (uint64_t)__shfl_xor((unsigned long long)key, kWave - 1, kWave);
+    list = list > turned ? list : turned;
+#pragma unroll
+    for (int j = kWave / 2; j > 0; j /= 2) {
+      const uint64_t other = (uint64_t)__shfl_xor((unsigned long long)list, j, kWave);
+      list = (list > other) == !(lane & (uint32_t)j) ? list : other;
+    }
     least = lane_key(list, (int)top - 1);
   }
 };
@@ -106,7 +124,7 @@ struct Scores {
   float* top_logprob;
   float* sums;     // [rows][parts][4]: m, s, w
   uint64_t* keys;  // [rows][top][parts]
-  uint32_t rows, vocab, top, parts, part;  // part: logits of one, a multiple of kScoreWaves * kBatch
+  uint32_t rows, vocab, top, parts, part;  // part: logits of one, a multiple of a block's batches
 };
 
 template <bool F32>
@@ -119,26 +137,38 @@ __device__ __forceinline__ float logit_at(const Scores& a, uint64_t row, uint64_
 template <bool F32>
 __device__ __forceinline__ void finish(const Scores& a, uint32_t row, const Sums3& t, const Best& best) {
   const uint32_t lane = (uint32_t)lane_id();
-  const float log_s = __builtin_amdgcn_logf(t.s) * kLn2, off = t.m == -INFINITY ? 0.0f : t.m;
+  const float log_s = __builtin_amdgcn_logf(t.s), off = t.m == -INFINITY ? 0.0f : t.m;
   const bool bad = t.s != t.s;
+  auto log_of = [&](float x) __attribute__((always_inline)) {
+    return x == -INFINITY ? -INFINITY : ((x - off) * kLog2e - log_s) * kLn2;
+  };
   if (lane == 0) {
     const int64_t token = a.tokens[row];
     const bool in = (uint64_t)token < (uint64_t)a.vocab;
-    const float x = in ? logit_at<F32>(a, row, (uint64_t)token) : NAN;
-    a.logprob[row] = bad || !in ? NAN : x == -INFINITY ? -INFINITY : x - off - log_s;
-    a.entropy[row] = bad ? NAN : t.s == 0.0f ? 0.0f : log_s - t.w / t.s;
+    a.logprob[row] = bad || !in ? NAN : log_of(logit_at<F32>(a, row, in ? (uint64_t)token : 0u));
+    a.entropy[row] = bad ? NAN : t.s == 0.0f ? 0.0f : (log_s - t.w / t.s) * kLn2;
   }
   if (lane < a.top) {
     const uint64_t at = (uint64_t)row * a.top + lane;
     a.ids[at] = best.list ? (int32_t)key_index(best.list) : -1;
-    a.top_logprob[at] = best.list ? (bad ? NAN : key_value(best.list) - off - log_s) : -INFINITY;
+    a.top_logprob[at] = best.list ? (bad ? NAN : log_of(key_value(best.list))) : -INFINITY;
   }
 }
 
-template <bool F32, bool TOP>
-__global__ __launch_bounds__(kWave* kScoreWaves) void k_token_logprobs(Scores a) {
-  __shared__ uint64_t room[kScoreWaves][2 * kWave];
-  __shared__ float sums[kScoreWaves][3];
+// One pass: a wave takes every NW-th batch of its part of the row, keeps the sums per
+// lane and the largest `top` keys in its lanes.  Without alternatives it is bound by
+// memory: 2048 rows of 100000 BF16 logits in 78 us, 5.2 TB/s (100003, whose rows start at
+// any 2-byte address: 89).  With 20 of them it is bound by instructions, 326 for a
+// batch of 16 logits per lane, of which the sums are 145 and the keys the rest: 120 us
+// (100003: 131; from HBM 147).  That keys are found in a batch is likely throughout, as
+// each wave has a list of its own; the waves share the least value that counts.  One or
+// two waves to a row find fewer but wait for their loads (152 and 149 us), and loads two
+// batches ahead took longer (164).
+template <bool F32, bool TOP, uint32_t NW>
+__global__ __launch_bounds__(kWave* NW) void k_token_logprobs(Scores a) {
+  __shared__ uint64_t room[NW][2 * kWave];
+  __shared__ float sums[NW][3];
+  __shared__ float shared_least;  // some wave has `top` keys of this value or larger ones
   const uint32_t lane = (uint32_t)lane_id(), wave = (uint32_t)wave_in_block();
   const uint32_t row = blockIdx.x / a.parts, part = blockIdx.x - row * a.parts;
   const uint32_t from = part * a.part;  // below vocab (cut_scores)
@@ -174,68 +204,86 @@ __global__ __launch_bounds__(kWave* kScoreWaves) void k_token_logprobs(Scores a)
   Sums3 t;
   Best best;
   best.top = a.top;
-  bool begun = false;
-  float least = -INFINITY;
+  if constexpr (TOP) {
+    if (threadIdx.x == 0) shared_least = -INFINITY;
+    __syncthreads();
+  }
+  volatile float* const others = &shared_least;
+  float least = -INFINITY;  // larger ones may be among the best
   auto use = [&](uint32_t at, const float x[kMine]) __attribute__((always_inline)) {
     float top = x[0];
 #pragma unroll
     for (int i = 1; i < kMine; ++i) top = fmaxf(top, x[i]);
     t.add(x, top);
     if constexpr (TOP) {
-      if (!begun) {
-        // at least `top` keys are as large as the top-th of the lanes' largest
-        uint64_t mine = 0;
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const uint64_t k = x[i] == -INFINITY ? 0u : key_of(x[i], index(at, i));
-          mine = k > mine ? k : mine;
-        }
-        Best lanes;
-        lanes.top = a.top;
-        lanes.start(mine, room[wave]);
+      const bool nan = t.s != t.s;
+      if (!best.least) {  // fewer than `top` so far
+        // at least `top` logits are as large as the top-th of the lanes' largest
+        const float enough = __int_as_float(
+            __builtin_amdgcn_readlane(__float_as_int(wave_sorted(__ballot(nan) ? -INFINITY : top)), (int)a.top - 1));
         uint32_t n = 0;
-        uint64_t first = 0;
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-          const uint64_t k = x[i] == -INFINITY ? 0u : key_of(x[i], index(at, i));
-          const bool take = k && k >= lanes.least;
+          const bool take = !(x[i] < enough) && x[i] != -INFINITY;
           const uint64_t mask = __ballot(take);
+          if (!mask) continue;
           const uint32_t to = n + (uint32_t)__popcll(mask & ((1ull << lane) - 1ull));
-          if (take && to < kWave) room[wave][to] = k;
+          if (take && to < kWave) room[wave][to] = key_of(x[i], index(at, i));
           n += (uint32_t)__popcll(mask);
         }
         wave_lds_sync();
-        first = lane < n ? room[wave][lane] : 0u;
+        const uint64_t first = lane < n ? room[wave][lane] : 0u;
         wave_lds_sync();
-        best.start(first, room[wave]);
-        if (n > kWave) {  // many equal ones
+        best.merge(first);
+        if (n > (uint32_t)kWave) {  // many equal ones
           uint32_t m = 0;
 #pragma unroll 1
           for (int i = 0; i < kMine; ++i) {
             float y = x[0];
 #pragma unroll
             for (int j = 1; j < kMine; ++j) y = i == j ? x[j] : y;
-            const uint64_t k = y == -INFINITY ? 0u : key_of(y, index(at, i));
-            const bool take = k && k >= lanes.least;
-            const uint64_t mask = __ballot(take);
+            const bool take = !(y < enough) && y != -INFINITY;
+            const uint64_t mask = __ballot(take), k = key_of(y, index(at, i));
             const uint32_t to = m + (uint32_t)__popcll(mask & ((1ull << lane) - 1ull));
             m += (uint32_t)__popcll(mask);
-            best.insert(k, __ballot(take && to >= kWave && k > best.least));
+            best.insert(k, __ballot(take && to >= (uint32_t)kWave && k > best.least));
           }
         }
-        begun = true;
-      } else if (__ballot(top > least || t.s != t.s)) {
+      } else if (__ballot(top > least || nan)) {
+        uint32_t n = 0;
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const bool take = !(x[i] <= least);
-          if (__ballot(take)) {
+        for (int g = 0; g < kMine; g += 4) {
+          bool any = false;
+#pragma unroll
+          for (int i = g; i < g + 4; ++i) any = any || !(x[i] <= least);
+          if (!__ballot(any)) continue;
+#pragma unroll
+          for (int i = g; i < g + 4; ++i) {
+            const bool take = !(x[i] <= least);
+            const uint64_t mask = __ballot(take);
+            if (!mask) continue;
             const uint64_t k = key_of(x[i], index(at, i));
-            best.insert(k, __ballot(take && k > best.least));
+            const uint32_t to = n + (uint32_t)__popcll(mask & ((1ull << lane) - 1ull));
+            if (take && to < (uint32_t)kWave) room[wave][to] = k;
+            n += (uint32_t)__popcll(mask);
+            if (n > (uint32_t)kWave) best.insert(k, __ballot(take && to >= (uint32_t)kWave && k > best.least));
           }
         }
+        wave_lds_sync();
+        const uint64_t k = lane < n ? room[wave][lane] : 0u;
+        wave_lds_sync();
+        if (n <= kSingly)
+          best.insert(k, __ballot(k > best.least));
+        else
+          best.merge(k);
       }
-      // keys that follow have larger indices: equal values are no better
-      least = best.least ? key_value(best.least) : -INFINITY;
+      // Keys that follow have larger indices than the wave's own: equal values are no
+      // better.  Of equal values of another wave they may have lower ones.
+      const float mine = best.least ? key_value(best.least) : -INFINITY, other = *others;
+      if (lane == 0 && mine > other) *others = mine;  // any wave's will do
+      const int32_t below = __float_as_int(other) + (other > 0.0f ? -1 : 1);  // the next lower number
+      least = other > -INFINITY && other != 0.0f ? fmaxf(mine, __int_as_float(below)) : mine;
+      least = mine != mine ? mine : least;
     }
   };
 
@@ -244,8 +292,8 @@ __global__ __launch_bounds__(kWave* kScoreWaves) void k_token_logprobs(Scores a)
     Slot now;
     load(at, now);
     while (at + kBatch <= end) {
-      const uint32_t next = at + kScoreWaves * kBatch;
-      Slot s = now;
+      const uint32_t next = at + NW * kBatch;
+      const Slot s = now;
       if (next + kBatch <= end) load(next, now);
       float x[kMine];
       values(s, x);
@@ -273,10 +321,10 @@ __global__ __launch_bounds__(kWave* kScoreWaves) void k_token_logprobs(Scores a)
   __syncthreads();
   if (wave) return;
 #pragma unroll
-  for (uint32_t i = 1; i < kScoreWaves; ++i) t.join(sums[i][0], sums[i][1], sums[i][2]);
+  for (uint32_t i = 1; i < NW; ++i) t.join(sums[i][0], sums[i][1], sums[i][2]);
   if constexpr (TOP) {
 #pragma unroll
-    for (uint32_t i = 1; i < kScoreWaves; ++i) {
+    for (uint32_t i = 1; i < NW; ++i) {
       const uint64_t k = room[i][kWave + lane];
       best.insert(k, __ballot(k > best.least));
     }
@@ -297,7 +345,6 @@ __global__ __launch_bounds__(kWave* kScoreWaves) void k_token_logprobs(Scores a)
 // The parts of a row, joined by one wave.
 template <bool F32>
 __global__ __launch_bounds__(kWave) void k_join_logprobs(Scores a) {
-  __shared__ uint64_t room[kWave];
   const uint32_t lane = (uint32_t)lane_id(), row = blockIdx.x;
   Sums3 t;
   if (lane < a.parts) {  // parts <= kWave
@@ -311,7 +358,7 @@ __global__ __launch_bounds__(kWave) void k_join_logprobs(Scores a) {
   best.top = a.top;
   const uint32_t n = a.top * a.parts;
   const uint64_t* const keys = a.keys + (uint64_t)row * n;  // the parts' best first
-  if (n) best.start(lane < n ? keys[lane] : 0u, room);
+  if (n) best.merge(lane < n ? keys[lane] : 0u);
   for (uint32_t i = kWave; i < n; i += kWave) {
     const uint64_t k = i + lane < n ? keys[i + lane] : 0u;
     best.insert(k, __ballot(k > best.least));
@@ -321,31 +368,46 @@ __global__ __launch_bounds__(kWave) void k_join_logprobs(Scores a) {
 
 namespace {
 
-// Rows are split where there are too few for the card: into parts of whole batches.
-int cut_scores(const wc_logprob_shape* s, uint32_t* parts, uint32_t* part) {
+// Enough rows to fill the card have a block of four waves each.  Fewer have one of 16,
+// up to eight batches a wave, in one launch (4 rows of 32000: 13.6 us and 12.4 of host
+// time; split and joined 12.7 and 17.1), and longer ones are split into parts
+// of whole batches and joined.
+struct ScoreCut {
+  uint32_t waves, parts, part;
+};
+int cut_scores(const wc_logprob_shape* s, ScoreCut* cut) {
   if (!s || s->vocab < 1u || s->vocab >= (1u << 31)) return WC_E_ARG;
   if (s->kind > WC_LOGITS_F32) return WC_E_ARG;
   if (s->top > WC_LOGPROB_MAX_TOP) return WC_E_UNSUPPORTED;
-  const uint32_t step = kScoreWaves * kBatch, steps = (s->vocab + step - 1u) / step;
-  uint32_t n = s->rows ? (4u * cu_count() + s->rows - 1u) / s->rows : 1u;
+  const uint32_t step = kManyWaves * kBatch, steps = (s->vocab + step - 1u) / step;
+  const bool few = s->rows < 2u * cu_count() && s->vocab <= kFewWaves * kBatch * 8u;
+  uint32_t n = s->rows && !few ? (4u * cu_count() + s->rows - 1u) / s->rows : 1u;
   n = n < (uint32_t)kWave ? n : (uint32_t)kWave;
   n = n < steps ? n : steps;
-  *part = (steps + n - 1u) / n * step;
-  *parts = (s->vocab - 1u) / *part + 1u;
-  if ((uint64_t)s->rows * *parts >= (1ull << 24)) return WC_E_SIZE;  // a grid of fewer than 2^32 threads
+  cut->waves = few ? kFewWaves : kManyWaves;
+  cut->part = (steps + n - 1u) / n * step;
+  cut->parts = (s->vocab - 1u) / cut->part + 1u;
+  if ((uint64_t)s->rows * cut->parts >= (1ull << 24)) return WC_E_SIZE;  // a grid of fewer than 2^32 threads
   return WC_OK;
 }
 uint64_t score_bytes(const wc_logprob_shape* s, uint32_t parts) {
   return parts == 1u ? 0u : (uint64_t)s->rows * parts * (16u + 8u * s->top);
 }
 
-template <bool F32>
-void launch_scores(const Scores& a, hipStream_t s) {
+template <bool F32, bool TOP>
+void launch_scores_of(const Scores& a, uint32_t waves, hipStream_t s) {
   const uint32_t blocks = a.rows * a.parts;
-  if (a.top)
-    k_token_logprobs<F32, true><<<blocks, kWave * kScoreWaves, 0, s>>>(a);
+  if (waves == kFewWaves)
+    k_token_logprobs<F32, TOP, kFewWaves><<<blocks, kWave * kFewWaves, 0, s>>>(a);
   else
-    k_token_logprobs<F32, false><<<blocks, kWave * kScoreWaves, 0, s>>>(a);
+    k_token_logprobs<F32, TOP, kManyWaves><<<blocks, kWave * kManyWaves, 0, s>>>(a);
+}
+template <bool F32>
+void launch_scores(const Scores& a, uint32_t waves, hipStream_t s) {
+  if (a.top)
+    launch_scores_of<F32, true>(a, waves, s);
+  else
+    launch_scores_of<F32, false>(a, waves, s);
   if (a.parts > 1u) k_join_logprobs<F32><<<a.rows, kWave, 0, s>>>(a);
 }
 
@@ -353,16 +415,16 @@ void launch_scores(const Scores& a, hipStream_t s) {
 }  // namespace wc
 
 extern "C" size_t wc_token_logprobs_workspace_bytes(const wc_logprob_shape* shape) {
-  uint32_t parts, part;
-  if (wc::cut_scores(shape, &parts, &part)) return 0;
-  return wc::score_bytes(shape, parts);
+  wc::ScoreCut cut;
+  if (wc::cut_scores(shape, &cut)) return 0;
+  return wc::score_bytes(shape, cut.parts);
 }
 
 extern "C" int wc_token_logprobs(const wc_logprob_shape* shape, const void* d_logits, const int64_t* d_tokens,
                                  float* d_logprobs, float* d_entropy, int32_t* d_top_ids, float* d_top_logprobs,
                                  void* d_work, size_t work_bytes, void* stream) {
-  uint32_t parts, part;
-  if (const int v = wc::cut_scores(shape, &parts, &part)) return v;
+  wc::ScoreCut cut;
+  if (const int v = wc::cut_scores(shape, &cut)) return v;
   const bool f32 = shape->kind == WC_LOGITS_F32;
   if (shape->stride >= (1ull << 40)) return WC_E_SIZE;
   if (shape->rows > 1u && shape->stride < shape->vocab) return WC_E_ARG;
@@ -371,7 +433,7 @@ extern "C" int wc_token_logprobs(const wc_logprob_shape* shape, const void* d_lo
   if (!d_logprobs || ((uintptr_t)d_logprobs & 3u) || !d_entropy || ((uintptr_t)d_entropy & 3u)) return WC_E_ARG;
   if (shape->top && (!d_top_ids || ((uintptr_t)d_top_ids & 3u) || !d_top_logprobs || ((uintptr_t)d_top_logprobs & 3u)))
     return WC_E_ARG;
-  const uint64_t need = wc::score_bytes(shape, parts);
+  const uint64_t need = wc::score_bytes(shape, cut.parts);
   if (need) {
     if (!d_work || !wc::aligned16(d_work)) return WC_E_ARG;
     if (work_bytes < need) return WC_E_SIZE;
@@ -385,15 +447,15 @@ extern "C" int wc_token_logprobs(const wc_logprob_shape* shape, const void* d_lo
   a.ids = d_top_ids;
   a.top_logprob = d_top_logprobs;
   a.sums = (float*)d_work;
-  a.keys = (uint64_t*)((uint8_t*)d_work + (uint64_t)shape->rows * parts * 16u);
+  a.keys = (uint64_t*)((uint8_t*)d_work + (uint64_t)shape->rows * cut.parts * 16u);
   a.rows = shape->rows;
   a.vocab = shape->vocab;
   a.top = shape->top;
-  a.parts = parts;
-  a.part = part;
+  a.parts = cut.parts;
+  a.part = cut.part;
   if (f32)
-    wc::launch_scores<true>(a, (hipStream_t)stream);
+    wc::launch_scores<true>(a, cut.waves, (hipStream_t)stream);
   else
-    wc::launch_scores<false>(a, (hipStream_t)stream);
+    wc::launch_scores<false>(a, cut.waves, (hipStream_t)stream);
   return hipGetLastError() == hipSuccess ? WC_OK : WC_E_HIP;
 }

@@ -107,12 +107,13 @@ def test_rows(rows, kind):
     check(*logits(rows, 4500, kind, seed=3), 4)
     if rows < 100:
         check(*logits(rows, 100003, kind, seed=4), 8)
+        check(*logits(rows, 140001, kind, seed=4), 8)
 
 
 @pytest.mark.parametrize("kind", KINDS)
 def test_ties_go_to_the_lowest_index(kind):
     dtype = torch.float32 if kind == "f32" else torch.bfloat16
-    for rows, vocab in ((2, 20000), (1500, 3000), (1, 70)):
+    for rows, vocab in ((2, 20000), (1500, 3000), (1, 70), (600, 9000), (2, 140000)):
         x = torch.zeros(rows, vocab, dtype=dtype, device=DEV)
         check(x, [vocab - 1] * rows, 20)
         x[:, 1::2] = -0.0  # equal to 0
@@ -223,7 +224,8 @@ def test_offsets_past_32_bits():
 
 def test_a_workspace_of_the_callers():
     x, tokens = logits(3, 40000, "f32", seed=12)
-    need = wc.token_logprobs_workspace_bytes(3, 40000, 9)
+    x, tokens = logits(3, 140000, "f32", seed=12)
+    need = wc.token_logprobs_workspace_bytes(3, 140000, 9)
     assert need > 0
     work = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device=DEV)
     check(x, tokens, 9, work=work)
@@ -231,9 +233,9 @@ def test_a_workspace_of_the_callers():
     assert wc.token_logprobs_workspace_bytes(3000, 40000, 9) == 0
 
 
-@pytest.mark.parametrize("rows", [3, 1200])
-def test_repeats_its_bits_on_streams_and_in_graphs(rows):
-    x, tokens = logits(rows, 9001, "f32", seed=13)
+@pytest.mark.parametrize("rows,vocab", [(3, 9001), (1200, 9001), (2, 150001)])
+def test_repeats_its_bits_on_streams_and_in_graphs(rows, vocab):
+    x, tokens = logits(rows, vocab, "f32", seed=13)
     t = torch.as_tensor(tokens, device=DEV)
     ref = [v.clone() for v in wc.token_logprobs(x, t, 6)]
     side = torch.cuda.Stream()

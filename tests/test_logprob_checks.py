@@ -129,7 +129,7 @@ P = 1 << 20  # a pointer that is aligned, and never followed
 
 
 def abi(logits=P, tokens=P, lp=P, entropy=P, ids=P, best=P, work=P, size=1 << 30, **more):
-    s = {"stride": 9000, "rows": 7, "vocab": 9000, "kind": 1, "top": 3, **more}
+    s = {"stride": 200000, "rows": 7, "vocab": 200000, "kind": 1, "top": 3, **more}
     shape = wc.LogprobShape(*(s[n] for n, _ in wc.LogprobShape._fields_))
     need = wc._lib.wc_token_logprobs_workspace_bytes(ctypes.byref(shape))
     return need, wc._lib.wc_token_logprobs(ctypes.byref(shape), logits, tokens, lp, entropy, ids, best, work,
@@ -143,7 +143,7 @@ def test_abi():
     for more, code in [({"vocab": 0}, -1), ({"vocab": 1 << 31}, -1), ({"kind": 2}, -1), ({"top": 33}, -5),
                        ({"rows": 1 << 24}, -2)]:
         assert abi(**more) == (0, code), more
-    for more, code in [({"stride": 8999}, -1), ({"stride": 1 << 40}, -2), ({"logits": None}, -1), ({"logits": P + 2}, -1),
+    for more, code in [({"stride": 199999}, -1), ({"stride": 1 << 40}, -2), ({"logits": None}, -1), ({"logits": P + 2}, -1),
                        ({"logits": P + 1, "kind": 0}, -1), ({"tokens": None}, -1), ({"tokens": P + 4}, -1),
                        ({"lp": None}, -1), ({"lp": P + 2}, -1), ({"entropy": None}, -1), ({"entropy": P + 1}, -1),
                        ({"ids": None}, -1), ({"ids": P + 2}, -1), ({"best": None}, -1), ({"best": P + 2}, -1),

@@ -213,6 +213,22 @@ def test_long(length, new):
     Case([length, 7, length // 3], new, 4, 2, 128, 64, seed=3).check()
 
 
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("heads,kv,new", [(4, 2, 1), (3, 1, 7)])
+def test_sequences_in_several_blocks(dim, heads, kv, new):
+    """Sequences that are split and joined, beside one that is not and an empty one."""
+    Case([2300, 0, 40, 1200], new, heads, kv, dim, 64, seed=14).check()
+
+
+@pytest.mark.parametrize("seqs", [63, 64, 65, 130])
+@pytest.mark.parametrize("window", [0, 2500])
+def test_many_sequences_in_several_blocks(seqs, window):
+    """More sequences than a wave has lanes, the long ones among the last."""
+    lengths = [int(x) for x in np.random.default_rng(15).integers(0, 60, seqs)]
+    lengths[-1], lengths[-3], lengths[seqs // 2] = 3000, 2600, 2200
+    Case(lengths, 1, 2, 1, 32, 64, seed=15).check(window=window)
+
+
 @pytest.mark.parametrize("window", [0, 700])
 def test_many_sequences(window):
     lengths = [int(x) for x in np.random.default_rng(4).integers(0, 900, 70)]
@@ -322,6 +338,23 @@ def test_pages_outside_the_cache_give_nan():
     assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
 
 
+def test_nan_in_sequences_of_several_blocks():
+    """A NaN key and a NaN value in the middle of a long sequence, a page that is not
+    there in another: all their queries; the third sequence keeps its bits."""
+    c = Case([2500, 2500, 2400], 2, 4, 2, 64, 64, seed=16)
+    clean, _ = c.run(c.cache())
+    for what in ("k", "v"):
+        cache = c.cache()
+        spoil(c, cache, 0, 1100, what, 0)
+        table = c.table.copy()
+        c.table[1, 20] = c.pages + 5
+        out, lse = c.run(cache)
+        c.table = table
+        assert bool(torch.isnan(out[0, :, :2]).all()) and torch.equal(out[0, :, 2:], clean[0, :, 2:])
+        assert bool(torch.isnan(out[1]).all()) and bool(torch.isnan(lse[1]).all())
+        assert torch.equal(out[2], clean[2])
+
+
 def test_lengths_past_the_table_give_nan():
     c = Case([64, 64], 3, 4, 2, 64, seed=10)
     cache = c.cache()
@@ -357,8 +390,9 @@ def test_offsets_past_32_bits():
 
 
 @pytest.mark.parametrize("new", [1, 6])
-def test_repeats_its_bits_on_streams_and_in_graphs(new):
-    c = Case([900, 33, 450], new, 8, 2, 128, 64, seed=12)
+@pytest.mark.parametrize("length", [900, 4000])
+def test_repeats_its_bits_on_streams_and_in_graphs(new, length):
+    c = Case([length, 33, 450], new, 8, 2, 128, 64, seed=12)
     cache = c.cache()
     ref = [t.clone() for t in c.run(cache)]
     side = torch.cuda.Stream()

@@ -230,3 +230,18 @@ def test_repeats_its_bits_on_streams_and_in_graphs(dim):
         torch.cuda.synchronize()
         want = wc.prompt_attention(q, k, v, s)
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_a_first_call_that_is_captured():
+    """Head dims whose blocks need more than 64 KB of LDS, first called in a graph."""
+    c = Case([100, 61], 2, 1, 224, seed=14)
+    q, k, v, s = dev16(c.q), dev16(c.k), dev16(c.v), starts_of(c.lengths)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = wc.prompt_attention(q, k, v, s)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        want = wc.prompt_attention(q, k, v, s)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])

@@ -67,6 +67,16 @@ struct Place {
   __device__ static __forceinline__ uint32_t value(uint32_t row) { return row / kRowsPerBank << 2 & kMask; }
 };
 
+// 16384 tokens, 32 heads of 128: 2.0 ms, 1100 TFLOP/s (a library product of 8192^3:
+// 1235), with the matrix cores busy half of the time at the 2.0 GHz that the card then
+// keeps; the rest is exponentials (141 vector instructions for 32 products) and waiting
+// for operands and for the other wave of the SIMD.  Operands are read a group of four
+// products ahead, and the products of the two halves of a tile alternate, as one waits
+// for the one before it on the same sums (chained: 2.1 ms).  Weights of one half between
+// the products of the other took longer (2.1 ms), as did three tiles in LDS (2.04) and
+// waves of other priorities (no change).  Blocks of 8 waves where sequences have 4096
+// tokens or more on average (2.01 ms; of 4 waves, two to a compute unit, 2.08), else of 4
+// (12 prompts to 2048: 150 us against 165), whose rows are fewer past the diagonal.
 template <int G, int NW>
 __global__ __launch_bounds__(kWave* NW, G <= 4 ? 2 : 1) void k_prompt(Prompt a) {
   using P = Place<G>;

@@ -774,6 +774,8 @@ def _token_rows(t: torch.Tensor, what: str, heads: int | None, dim: int):
     if t.is_contiguous():
         return tokens, heads, stride
     strides = t.stride()
+    if len(shape) == 3 and tokens > 1 and strides[1:] == (dim, 1) and strides[0] >= stride and not strides[0] % 8:
+        return tokens, heads, strides[0]
     for n, s in zip(reversed(shape[:-2]), reversed(strides[:-2])):  # from the last to the first
         if n > 1 and tokens:
             if not step:

@@ -217,8 +217,12 @@ __global__ __launch_bounds__(kWave* NW) void k_token_logprobs(Scores a) {
     t.add(x, top);
     if constexpr (TOP) {
       const bool nan = t.s != t.s;
-      if (!best.least) {  // fewer than `top` so far
-        // at least `top` logits are as large as the top-th of the lanes' largest
+      // Fewer than `top` so far, or a batch in which half the lanes have better ones (rising
+      // rows): at least `top` of its logits are as large as the top-th of the lanes' largest.
+      // 2048 x 100003 BF16 that rise along the row, 20 alternatives: 676 us with this bar,
+      // 1581 with the list's least alone; random rows 133 with either.
+      const uint32_t lanes = (uint32_t)__popcll(__ballot(top > least));
+      if (!best.least || (lanes >= (uint32_t)kWave / 2 && lanes >= a.top && !__ballot(nan))) {
         const float enough = __int_as_float(
             __builtin_amdgcn_readlane(__float_as_int(wave_sorted(__ballot(nan) ? -INFINITY : top)), (int)a.top - 1));
         uint32_t n = 0;
@@ -249,7 +253,7 @@ __global__ __launch_bounds__(kWave* NW) void k_token_logprobs(Scores a) {
             best.insert(k, __ballot(take && to >= (uint32_t)kWave && k > best.least));
           }
         }
-      } else if (__ballot(top > least || nan)) {
+      } else if (lanes || __ballot(nan)) {
         uint32_t n = 0;
 #pragma unroll
         for (int g = 0; g < kMine; g += 4) {

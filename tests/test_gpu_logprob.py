@@ -129,6 +129,20 @@ def test_ties_go_to_the_lowest_index(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("top", [1, 20, 32])
+def test_rising_rows(kind, top):
+    """Every batch of a row holds more values above the list's least than there is room for."""
+    dtype = torch.float32 if kind == "f32" else torch.bfloat16
+    for rows, vocab in ((2, 50003), (1200, 20000)):
+        g = torch.Generator().manual_seed(top)
+        at = torch.arange(vocab).float().div(vocab).expand(rows, -1)
+        noise = torch.randn(rows, vocab, generator=g)
+        for x in (12 * at, 12 * at + noise / 64, 12 * at + noise, 6 * at * noise,
+                  torch.where(torch.arange(vocab) % 3 == 0, 12 * at, float("-inf"))):
+            check(x.to(dtype).to(DEV), [vocab - 2] * rows, top)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_masked_tokens(kind):
     for rows, vocab in ((3, 20000), (1500, 3000)):
         x, tokens = logits(rows, vocab, kind, seed=5)

@@ -193,8 +193,10 @@ __global__ __launch_bounds__(kWave* NW, G <= 4 ? 2 : 1) void k_prompt(Prompt a) 
     const bool edge = t0 + kStepTokens - 1u > w0 || (a.window && w1 >= a.window && t0 <= w1 - a.window);
     mfma_f32x16 s[2];
     float part;
-    bool need = m == -INFINITY, full = __ballot(need);
-    for (;;) {  // once more where a query's offset has to move
+    // Each query goes by its own sums alone: one that has no score to take as its offset
+    // (NaN, or -inf throughout) does not keep the others from moving theirs.
+    bool need = m == -INFINITY, set = false, full = __ballot(need);
+    for (;;) {  // once more where a query's offset has to move, which it does at most once
       // operands a group of four products ahead
       u32x4 keys[2][4];
       auto load_keys = [&](auto j) __attribute__((always_inline)) {
@@ -232,6 +234,7 @@ __global__ __launch_bounds__(kWave* NW, G <= 4 ? 2 : 1) void k_prompt(Prompt a) 
         const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(off - to);
         m = now;
         off = to;
+        set = set || need;
         sum *= f;
         each<G>([&](auto g) __attribute__((always_inline)) { acc[g] *= f; });
       }
@@ -242,8 +245,7 @@ __global__ __launch_bounds__(kWave* NW, G <= 4 ? 2 : 1) void k_prompt(Prompt a) 
           part += s[t][+i];
         });
       });
-      if (full) break;
-      need = !(part <= kMost);
+      need = !set && !(part <= kMost);
       full = __ballot(need);
       if (!full) break;
       const int other = __shfl_xor((int)need, 32, kWave);

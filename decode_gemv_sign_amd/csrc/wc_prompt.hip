@@ -394,9 +394,11 @@ extern "C" int wc_prompt_attention(const wc_prompt_shape* shape, const uint16_t*
     return WC_E_ARG;
   // a factor that makes every score 0 without making a mask's infinity NaN
   const float scale = s.scale == 0.0f ? 1e-37f : s.scale * wc::kLog2e;
-  const wc::Prompt a = {d_q, d_k, d_v, d_starts, d_out, d_lse, s.tokens, (uint32_t)s.q_stride, (uint32_t)s.k_stride,
-                        (uint32_t)s.v_stride, s.seqs, s.heads, s.kv_heads, s.heads / s.kv_heads, s.window,
-                        scale, scale < 0.0f ? INFINITY : -INFINITY};
+  // the strides are the lengths of the buffers' rows too: those of one token may be anything
+  const bool one = s.tokens == 1u;
+  const wc::Prompt a = {d_q, d_k, d_v, d_starts, d_out, d_lse, s.tokens, (uint32_t)s.q_stride,
+                        (uint32_t)(one ? kv_row : s.k_stride), (uint32_t)(one ? kv_row : s.v_stride), s.seqs, s.heads,
+                        s.kv_heads, s.heads / s.kv_heads, s.window, scale, scale < 0.0f ? INFINITY : -INFINITY};
   const hipStream_t st = (hipStream_t)stream;
   switch (s.head_dim / 32u) {
     case 1: return wc::launch_prompt_of<1>(a, shape, st);

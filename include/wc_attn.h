@@ -104,7 +104,8 @@ int wc_fp4_attention(const wc_fp4_cache *cache, const wc_fp4_attention_shape *sh
 
 typedef struct wc_prompt_shape {
   uint64_t tokens;                       /* of all prompts */
-  uint64_t q_stride, k_stride, v_stride; /* elements from one token to the next, below 2^24 */
+  uint64_t q_stride, k_stride, v_stride; /* elements from one token to the next, below 2^24 (of one
+                                            token alone: any multiple of 8) */
   uint32_t seqs;
   uint32_t heads, kv_heads, head_dim;
   uint32_t window; /* 0: none */

@@ -1,0 +1,31 @@
+"""Calls of the prompt attention at the edges of what its header allows."""
+import ctypes
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import decode_gemv_sign_amd as wc  # noqa: E402
+from tests.test_gpu_prompt import DEV, Case, dev16, starts_of  # noqa: E402
+
+
+@pytest.mark.parametrize("dim", [32, 64, 96, 128, 192, 256])
+@pytest.mark.parametrize("stride", [0, 8, 32, 64])
+def test_one_token_of_any_stride(dim, stride):
+    """Strides lie between tokens: of one token they say nothing."""
+    c = Case([1], 4, 2, dim, seed=31)
+    q, k, v = (dev16(x) for x in (c.q, c.k, c.v))
+    want, want_lse = wc.prompt_attention(q, k, v, starts_of([1]))
+    assert torch.equal(want[0].view(torch.int16), v[0].repeat_interleave(2, 0))
+    out, lse = torch.zeros_like(want), torch.zeros_like(want_lse)
+    shape = wc.PromptShape(1, stride, stride, stride, 1, 4, 2, dim, 0, dim ** -0.5)
+    assert wc._lib.wc_prompt_attention(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                       starts_of([1]).data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                       torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)

@@ -392,8 +392,9 @@ extern "C" int wc_prompt_attention(const wc_prompt_shape* shape, const uint16_t*
   if (!d_q || !wc::aligned16(d_q) || !d_k || !wc::aligned16(d_k) || !d_v || !wc::aligned16(d_v)) return WC_E_ARG;
   if (!d_starts || ((uintptr_t)d_starts & 3u) || !d_out || !wc::aligned16(d_out) || ((uintptr_t)d_lse & 3u))
     return WC_E_ARG;
-  // a factor that makes every score 0 without making a mask's infinity NaN
-  const float scale = s.scale == 0.0f ? 1e-37f : s.scale * wc::kLog2e;
+  // a factor that makes every score 0 without making a mask's infinity NaN: fp32's least number
+  // (the largest score then counts as 2^-21)
+  const float scale = s.scale == 0.0f ? 0x1p-149f : s.scale * wc::kLog2e;
   // the strides are the lengths of the buffers' rows too: those of one token may be anything
   const bool one = s.tokens == 1u;
   const wc::Prompt a = {d_q, d_k, d_v, d_starts, d_out, d_lse, s.tokens, (uint32_t)s.q_stride,

@@ -29,3 +29,24 @@ def test_one_token_of_any_stride(dim, stride):
                                        torch.cuda.current_stream().cuda_stream) == 0
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.0])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_scale_of_zero_of_large_scores(dim, scale):
+    """Every score is 0, however large the product: the mean of the values.  Scores of
+    2^118 dim and more differ from token to token."""
+    c = Case([200, 70], 2, 1, dim, seed=32)
+    small = c.run(scale=scale)
+    c.q = (c.q & 0x807F) | 0x5D80  # 2^60 and up, of either sign
+    c.k = (c.k & 0x807F) | 0x5C80  # 2^58 and up
+    got = c.run(scale=scale)
+    # The products are below 2^127: where the factor is fp32's least number, 2^-149, weights are
+    # within 2^-22 of 1, BF16 rounds them to 1, and the outputs are the same sums over a divisor
+    # off by 2^-22 at most: one step of BF16, in a rare tie.
+    near = (got[0].float() - small[0].float()).abs() <= 2.0 ** -7 * small[0].float().abs()
+    assert bool(near.all())
+    count = np.concatenate([np.arange(1, 201), np.arange(1, 71)])
+    want = torch.from_numpy(np.log(count)).to(DEV)[:, None]
+    # the sum is off by 2^-22 at most, its offset by as much, the logarithm by two of its steps
+    assert bool(((got[1].double() - want).abs() <= 2.0 ** -22 * (2 + want)).all())

@@ -769,7 +769,7 @@ def _token_rows(t: torch.Tensor, what: str, heads: int | None, dim: int):
     if len(shape) < 3 or shape[-1] != dim or shape[-2] < 1 or (heads is not None and shape[-2] != heads):
         raise ValueError(f"{what} has shape {shape}, expected [.., {'heads' if heads is None else heads}, {dim}]")
     heads = shape[-2]
-    stride, step = heads * dim, 0
+    stride, step = heads * dim, None
     tokens = t.numel() // stride
     if t.is_contiguous():
         return tokens, heads, stride
@@ -778,11 +778,11 @@ def _token_rows(t: torch.Tensor, what: str, heads: int | None, dim: int):
         return tokens, heads, strides[0]
     for n, s in zip(reversed(shape[:-2]), reversed(strides[:-2])):  # from the last to the first
         if n > 1 and tokens:
-            if not step:
+            if step is None:
                 stride = step = s
             elif s != step:
                 raise ValueError(f"{what}: tokens of strides {strides} are not one step apart")
-        step *= n
+            step *= n
     if tokens and (strides[-1] != 1 or (heads > 1 and strides[-2] != dim) or stride < heads * dim or stride % 8):
         raise ValueError(f"{what}: strides {strides}; a token's heads must be contiguous and tokens a multiple of 8 "
                          f"numbers apart")

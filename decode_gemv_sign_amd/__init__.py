@@ -965,10 +965,22 @@ def _logprob_need(lib, device, rows, vocab, f32, top) -> int:
     return lib.wc_token_logprobs_workspace_bytes(ctypes.byref(LogprobShape(vocab, rows, vocab, f32, top)))
 
 
+def _logprob_sizes(rows, vocab, top, dtype) -> bool:
+    """True for fp32 logits; what the library cannot take is refused."""
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("logits must be float32 or bfloat16")
+    if (rows | vocab) >> 31 or vocab < 1:
+        raise ValueError(f"rows {rows} or vocab {vocab} outside 0..2^31 - 1 (vocab from 1)")
+    if not 0 <= top <= LOGPROB_MAX_TOP:
+        raise ValueError(f"top {top} outside 0..{LOGPROB_MAX_TOP}")
+    return dtype == torch.float32
+
+
 def token_logprobs_workspace_bytes(rows: int, vocab: int, top: int = 0, dtype=torch.float32) -> int:
     """wc_token_logprobs_workspace_bytes: device scratch of one token_logprobs call
     of that shape on the current device (looked up once for each)."""
-    return _logprob_need(_lib, torch._C._cuda_getDevice(), rows, vocab, dtype == torch.float32, top)
+    f32 = _logprob_sizes(rows, vocab, top, dtype)
+    return _logprob_need(_lib, torch._C._cuda_getDevice(), rows, vocab, f32, top)
 
 
 def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, *, work: torch.Tensor | None = None,
@@ -984,16 +996,10 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, *, 
     stream must not overlap."""
     if not _on_device(logits):
         raise ValueError("logits must be a device tensor")
-    f32 = logits.dtype == torch.float32
-    if not f32 and logits.dtype != torch.bfloat16:
-        raise TypeError("logits must be float32 or bfloat16")
-    if logits.dim() != 2 or logits.shape[1] < 1:
+    if logits.dim() != 2:
         raise ValueError(f"logits must be [rows, vocab], got {tuple(logits.shape)}")
     rows, vocab = logits.shape
-    if (rows | vocab) >> 31:
-        raise ValueError(f"logits have shape {tuple(logits.shape)}: a size does not fit 31 bits")
-    if not 0 <= top <= LOGPROB_MAX_TOP:
-        raise ValueError(f"top {top} outside 0..{LOGPROB_MAX_TOP}")
+    f32 = _logprob_sizes(rows, vocab, top, logits.dtype)
     stride = logits.stride(0) if rows > 1 else vocab
     if (vocab > 1 and logits.stride(1) != 1) or stride < vocab:
         raise ValueError(f"logits of strides {logits.stride()}: a row must be contiguous and rows must not overlap")

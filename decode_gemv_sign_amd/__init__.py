@@ -805,7 +805,7 @@ def fp4_cache_append(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slot
     the slots (int64 [tokens]: page * page_size + place) of the cache, each group of
     32 numbers with a scale as by fp4_encode.  A token whose slot is outside the
     cache (-1) is left out; slots of one call must differ.  k and v may be slices
-    by heads of a wider tensor."""
+    by heads of a wider tensor, not broadcast over tokens."""
     c, heads, dim = _cache(cache)
     tokens, _, ks = _token_rows(k, "k", heads, dim)
     vt, _, vs = _token_rows(v, "v", heads, dim)
@@ -873,7 +873,9 @@ def fp4_attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, len
     (0: all).  heads is a multiple of the cache's; scale: head_dim ** -0.5.
 
     out BF16 like q, lse fp32 [.., heads]: the logarithm of the sum of the scores'
-    exponentials.  A query without any position gets 0 and -inf.  work: uint8,
+    exponentials.  A query without any position gets 0 and -inf.  q may be a slice by
+    heads of a wider tensor, not one that is broadcast over tokens.  Limits of sizes (WCError)
+    go by the table's width, not by the lengths: include/wc_attn.h.  work: uint8,
     fp4_attention_workspace_bytes(..) of it; a call with the same one on another
     stream must not overlap."""
     c, kv_heads, dim = _cache(cache)

@@ -789,9 +789,15 @@ int attn_cut(const wc_fp4_cache* c, const wc_fp4_attention_shape* s, Cut* cut) {
   const uint64_t all = tiles * s->seqs, rows = (uint64_t)c->kv_heads * cut->col_tiles;
   if (all >= (1ull << 30) || (uint64_t)s->seqs * s->new_tokens * s->heads >= (1ull << 24)) return WC_E_SIZE;
   // Whole sequences where a wave has at most four tiles of them and half of the card has
-  // a block (16 sequences of 1000 positions, 16 heads of 64: 9.2 us against 14.4 split
-  // and joined), or where it has one: a block alone draws little from memory (one
-  // sequence of 1500, 8 heads of 128: 12.7 us whole, 9.7 split).
+  // a block, or where it has one: a block alone draws little from memory.  us in a graph,
+  // whole / split and joined, 32 heads on 8 of 128:
+  //   whole by the rule   1 x 500 8.2 / 9.5, 16 x 1000 12.2 / 14.0, 16 x 2000 17.9 / 18.6,
+  //                       32 x 2000 20.0 / 25.5, 64 x 2000 38.8 / 36.1
+  //   split by the rule   1 x 1000 10.2 / 9.5, 1 x 1500 12.9 / 9.8, 1 x 2048 15.5 / 10.3,
+  //                       4 x 2000 15.8 / 11.4, 8 x 2000 16.2 / 14.3, 32 x 4000 34.1 / 37.1
+  // and 16 x 1000 of other head dims 7.1 / 10.9 (32), 8.3 / 11.5 (64), 13.7 / 16.1 (160),
+  // 15.7 / 18.1 (256).  The lengths are on the device, so the rule goes by what the table
+  // or the window allows: 16 x 1000 in a table of 2048 pages of 64 take the split, 14.6.
   const uint64_t waves = c->head_dim <= 128u ? 16u : 8u;
   cut->whole = tiles <= waves || (tiles <= 4u * waves && rows * s->seqs >= cu_count() / 2u);
   // four blocks to a compute unit (32 sequences to 8192: 27.2 us; three 28.6, two 32.1, six 29.1)

@@ -157,13 +157,13 @@ __device__ __forceinline__ void finish(const Scores& a, uint32_t row, const Sums
 
 // One pass: a wave takes every NW-th batch of its part of the row, keeps the sums per
 // lane and the largest `top` keys in its lanes.  Without alternatives it is bound by
-// memory: 2048 rows of 100000 BF16 logits in 78 us, 5.2 TB/s (100003, whose rows start at
-// any 2-byte address: 89).  With 20 of them it is bound by instructions, 326 for a
-// batch of 16 logits per lane, of which the sums are 145 and the keys the rest: 120 us
-// (100003: 131; from HBM 147).  That keys are found in a batch is likely throughout, as
-// each wave has a list of its own; the waves share the least value that counts.  One or
-// two waves to a row find fewer but wait for their loads (152 and 149 us), and loads two
-// batches ahead took longer (164).
+// memory: 2048 rows of 100000 BF16 logits in 86 us, 4.8 TB/s (100003, whose rows start at
+// any 2-byte address: 98; both in a graph, from HBM).  With 20 of them it is bound by
+// instructions, 320 vector ones for a batch of 16 logits per lane, 162 without
+// alternatives: 132 us (100003: 133 to 143).  That keys are found in a batch is likely
+// throughout, as each wave has a list of its own; the waves share the least value that
+// counts.  One or two waves to a row find fewer but wait for their loads (152 and 149 us
+// where this took 147), and loads two batches ahead took longer (164).
 template <bool F32, bool TOP, uint32_t NW>
 __global__ __launch_bounds__(kWave* NW) void k_token_logprobs(Scores a) {
   __shared__ uint64_t room[NW][2 * kWave];
@@ -220,7 +220,7 @@ __global__ __launch_bounds__(kWave* NW) void k_token_logprobs(Scores a) {
       // Fewer than `top` so far, or a batch in which half the lanes have better ones (rising
       // rows): at least `top` of its logits are as large as the top-th of the lanes' largest.
       // 2048 x 100003 BF16 that rise along the row, 20 alternatives: 676 us with this bar,
-      // 1581 with the list's least alone; random rows 133 with either.
+      // 1581 with the list's least alone; random rows took 133 in the same calls with either.
       const uint32_t lanes = (uint32_t)__popcll(__ballot(top > least));
       if (!best.least || (lanes >= (uint32_t)kWave / 2 && lanes >= a.top && !__ballot(nan))) {
         const float enough = __int_as_float(
@@ -373,9 +373,17 @@ __global__ __launch_bounds__(kWave) void k_join_logprobs(Scores a) {
 namespace {
 
 // Enough rows to fill the card have a block of four waves each.  Fewer have one of 16,
-// up to eight batches a wave, in one launch (4 rows of 32000: 13.6 us and 12.4 of host
-// time; split and joined 12.7 and 17.1), and longer ones are split into parts
-// of whole batches and joined.
+// up to eight batches a wave, in one launch, and longer ones are split into parts of whole
+// batches and joined by a second.  fp32, 5 alternatives, whole / split, us in a graph (from
+// Python; a second launch is 5 us of host time):
+//   logits        1 row                     4 rows      32 rows                  256 rows
+//   8000     9.3 / 11.0 (14 / 18)      9.8 / 11.5   10.1 / 12.2 (14 / 18)   11.3 / 14.6
+//   32000   13.5 / 11.0 (14 / 18)     14.3 / 11.8   15.5 / 13.1 (15 / 18)   18.1 / 22.5
+//   64000   17.3 / 11.5 (17 / 18)     18.0 / 12.2   19.0 / 14.6 (18 / 18)   22.7 / 26.7
+//   128256  23.3 / 11.8 (23 / 18)     24.1 / 13.1   25.5 / 17.5 (25 / 18)   32.3 / 34.8
+//   152064  24.8 / 12.0 (25 / 18)     26.0 / 13.4   27.5 / 20.6 (26 / 19)   36.4 / 39.8
+// So the limit of eight batches is right for calls from Python up to 64000 logits and for
+// 256 rows; in a graph, few rows past 16000 are faster split.
 struct ScoreCut {
   uint32_t waves, parts, part;
 };

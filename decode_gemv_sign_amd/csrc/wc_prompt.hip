@@ -45,6 +45,12 @@ struct Prompt {
 // and receive a column each).  The second product has the head's columns as rows,
 // so that the running maximum and sum of a query stay in its lane pair.
 //
+// That rounding of the weights (not of their sum) is as large as the outputs' own:
+// 2.3e-3 of the norm from 64 bits where fp32 weights are 1.7e-3 away.  Weights as the
+// sum of two BF16 numbers would close that, with half as many products more on the unit
+// that bounds the kernel: 16384 tokens 2.88 ms against 2.14 in the same run, 12 prompts
+// to 2048 172 us against 145.
+//
 // Weights are exp2(s - offset), the offset a value near the query's largest score so
 // far: it is set at its first tile, and moves (and the tile is done once more) only
 // when the weights of a tile add up to more than kMost.  So a step looks for no
@@ -67,16 +73,19 @@ struct Place {
   __device__ static __forceinline__ uint32_t value(uint32_t row) { return row / kRowsPerBank << 2 & kMask; }
 };
 
-// 16384 tokens, 32 heads of 128: 2.0 ms, 1100 TFLOP/s (a library product of 8192^3:
-// 1235), with the matrix cores busy half of the time at the 2.0 GHz that the card then
-// keeps; the rest is exponentials (141 vector instructions for 32 products) and waiting
-// for operands and for the other wave of the SIMD.  Operands are read a group of four
-// products ahead, and the products of the two halves of a tile alternate, as one waits
-// for the one before it on the same sums (chained: 2.1 ms).  Weights of one half between
-// the products of the other took longer (2.1 ms), as did three tiles in LDS (2.04) and
-// waves of other priorities (no change).  Blocks of 8 waves where sequences have 4096
-// tokens or more on average (2.01 ms; of 4 waves, two to a compute unit, 2.08), else of 4
-// (12 prompts to 2048: 150 us against 165), whose rows are fewer past the diagonal.
+// 16384 tokens, 32 heads of 128: 2.06 ms in a graph (1.97 to 2.2 from card to card and
+// run to run), 1066 TFLOP/s where a library product of 8192^3 reached 1184, with the
+// matrix cores busy half of the time at the 2.0 GHz that the card then keeps; the rest is
+// exponentials (141 vector instructions for 32 products) and waiting for operands and for
+// the other wave of the SIMD.  Operands are read a group of four products ahead, and the
+// products of the two halves of a tile alternate, as one waits for the one before it on
+// the same sums.  (Of runs at 2.0 ms: chained 2.1, weights of one half between the
+// products of the other 2.1, three tiles in LDS 2.04, waves of other priorities no
+// change.)  launch_prompt_of has the block shapes' figures.
+//
+// Head dims past 128 have one wave to a SIMD (up to 456 registers) and rows of 512 bytes in
+// LDS whatever their length: 16384 tokens of heads of 160 4.2 ms, 192 4.6, 224 5.0, 256
+// 5.6, at 655 to 790 TFLOP/s.
 template <int G, int NW>
 __global__ __launch_bounds__(kWave* NW, G <= 4 ? 2 : 1) void k_prompt(Prompt a) {
   using P = Place<G>;
@@ -365,6 +374,18 @@ int launch_prompt(const Prompt& a, const wc_prompt_shape* p, hipStream_t s) {
   return launched();
 }
 
+// Blocks of 8 waves (one to a compute unit) read keys and values half as often, of 4 (two)
+// have fewer rows past the diagonal.  32 heads on 8, us in a graph with 4 / 8 waves:
+//   head dim                 32          64          96          128
+//   1 x 16384 tokens      863 / 883  1240 / 1388  1883 / 1865  2176 / 2100
+//   3 x 8192              705 / 739   978 / 1181  1492 / 1540  1739 / 1689
+//   1 x 8192              234 / 247   336 / 380    480 / 509    563 / 564
+//   4 x 4096              271 / 293   363 / 428    535 / 576    629 / 641
+//   1 x 4096               79 / 92    100 / 110    145 / 142    169 / 157
+//   8 x 2048              144 / 157   188 / 237    272 / 300    310 / 336
+// The rule was made for heads of 128, where it gains up to 7% and loses up to 2.  From 4096
+// tokens on heads of 96 lie between a gain of 2% and a loss of 8, those of 32 and 64 lose 2
+// to 21.
 template <int G>
 int launch_prompt_of(const Prompt& a, const wc_prompt_shape* p, hipStream_t s) {
   if constexpr (G <= 4)

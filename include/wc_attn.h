@@ -13,8 +13,10 @@
  * are attended to and nowhere else.
  *
  * Scores, exponentials and sums are fp32; products of BF16 and 4-bit values are
- * exact.  out is rounded to BF16 once.  The sums' order is fixed by the shape and
- * the lengths: the same call gives the same bits.
+ * exact.  out is rounded to BF16 once; over a prompt the weights exp(s - lse), not
+ * their sum, are too.  The sums' order is fixed by the shape and the lengths: the same
+ * call gives the same bits.  Values are summed with weights of up to 2^16 before they are
+ * divided: values past 2^111 / tokens may overflow where the output itself would not.
  *
  * The cache is an array of pages, tiles of 32 tokens in each:
  *   uint8 [pages][kv_heads][page_size / 32][34 head_dim]
@@ -50,7 +52,7 @@ extern "C" {
 
 typedef struct wc_fp4_cache {
   uint8_t *d_data;
-  uint64_t pages;     /* 1 .. 2^31 - 1 */
+  uint64_t pages;     /* 1 .. 2^31 - 1; pages * page_size below 2^36 */
   uint32_t page_size; /* tokens, a multiple of 32 up to 2^20 */
   uint32_t kv_heads;  /* 1 .. WC_ATTN_MAX_HEADS */
   uint32_t head_dim;
@@ -64,7 +66,8 @@ typedef struct wc_fp4_cache {
  * v_stride elements from one token to the next, into the slots d_slots[tokens].
  * Rounded as by wc_fp4_encode.  A slot outside 0 .. pages * page_size - 1 leaves
  * its token out (-1 for a place that is not used).  Slots of one call must
- * differ: of a slot that is given twice the bytes may be either token's.
+ * differ: of a slot that is given twice the bytes may be either token's.  tokens and
+ * the strides are below 2^31 (WC_E_SIZE).
  */
 int wc_fp4_cache_append(const wc_fp4_cache *cache, const uint16_t *d_k, uint64_t k_stride,
                         const uint16_t *d_v, uint64_t v_stride, const int64_t *d_slots,
@@ -85,8 +88,8 @@ typedef struct wc_fp4_attention_shape {
   float scale;
 } wc_fp4_attention_shape;
 
-/* Device scratch of a call of that shape (0: none is needed).  Host only; asks
- * the current device for its size. */
+/* Device scratch of a call of that shape (0: none is needed, or the call refuses the
+ * shape).  Host only; asks the current device for its size. */
 size_t wc_fp4_attention_workspace_bytes(const wc_fp4_cache *cache, const wc_fp4_attention_shape *shape);
 
 /*
@@ -97,6 +100,14 @@ size_t wc_fp4_attention_workspace_bytes(const wc_fp4_cache *cache, const wc_fp4_
  * d_lse fp32 [seqs * new_tokens][heads] or NULL.  Entries of the table past a
  * sequence's length, or before its window, are not used.  A query that attends to a
  * token whose page is outside the cache, or past the table, gets NaN.
+ *
+ * The sizes are those of the table, whatever the lengths.  WC_E_SIZE where
+ *   table_width * page_size is past 2^30,
+ *   seqs times the tiles of 32 tokens that a sequence may have (of the table, or that
+ *   a window may touch) is 2^30 or more,
+ *   seqs * new_tokens * heads is 2^24 or more,
+ *   kv_heads * ceil(new_tokens * heads / kv_heads / 16) * seqs is near 2^22 or more, or
+ *   q_stride is 2^31 or more.
  */
 int wc_fp4_attention(const wc_fp4_cache *cache, const wc_fp4_attention_shape *shape,
                      const uint16_t *d_q, const int32_t *d_table, const int32_t *d_lengths,
@@ -118,7 +129,8 @@ typedef struct wc_prompt_shape {
  * is the tokens d_starts[i] .. d_starts[i + 1] - 1, the first of them at position 0.
  * (Entries outside 0 .. tokens count as the nearer end.)  d_out BF16
  * [tokens][heads][head_dim], d_lse fp32 [tokens][heads] or NULL; tokens of no
- * sequence are left as they were.
+ * sequence are left as they were.  WC_E_SIZE where tokens or seqs is 2^31 or more, and
+ * possibly from (tokens / 128 + seqs) * heads = 2^23 on.
  */
 int wc_prompt_attention(const wc_prompt_shape *shape, const uint16_t *d_q, const uint16_t *d_k,
                         const uint16_t *d_v, const int32_t *d_starts, uint16_t *d_out, float *d_lse,

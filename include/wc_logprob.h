@@ -33,15 +33,15 @@ extern "C" {
 #define WC_LOGPROB_MAX_TOP 32u
 
 typedef struct wc_logprob_shape {
-  uint64_t stride; /* elements from one row to the next, at least vocab */
-  uint32_t rows;
+  uint64_t stride; /* elements from one row to the next, at least vocab, below 2^40 */
+  uint32_t rows;   /* below 2^24, else WC_E_SIZE */
   uint32_t vocab;  /* 1 .. 2^31 - 1 */
   uint32_t kind;   /* WC_LOGITS_BF16 or WC_LOGITS_F32 */
   uint32_t top;    /* 0 .. WC_LOGPROB_MAX_TOP, else WC_E_UNSUPPORTED */
 } wc_logprob_shape;
 
-/* Device scratch of a call of that shape (0: none is needed).  Host only; asks
- * the current device for its size. */
+/* Device scratch of a call of that shape (0: none is needed, or the call refuses the
+ * shape).  Host only; asks the current device for its size. */
 size_t wc_token_logprobs_workspace_bytes(const wc_logprob_shape *shape);
 
 /*
